@@ -83,6 +83,10 @@ typedef enum {
 #define DSPARK_DEV_TIMEOUT 0x8u      /* a bounded device wait ran out */
 #define DSPARK_DEV_BAD_VALUE 0x10u   /* calibration: a non-finite logit, or a grid entry that is no temperature */
 
+#define DSPARK_DEV_CACHE_FULL 0x20u   /* cache plan: a request got fewer tokens than it asked for (pages ran out) */
+#define DSPARK_DEV_PAGE_RANGE 0x40u   /* cache: a page or slot outside the pool (page 0 read, or the token skipped) */
+#define DSPARK_DEV_LENGTH_RANGE 0x80u /* cache: a length, row offset or count outside its range was clamped */
+
 /* Library version and the build's target (a string such as "sm_100a"). */
 const char *dspark_version(void);
 
@@ -370,6 +374,118 @@ dspark_status dspark_sts_fit(const float *z, const int32_t *acc, const float *ta
  *          Exact integers.  Needs no workspace; limits as dspark_sts_fit. */
 dspark_status dspark_survival_auc(const float *S, const int32_t *acc, int N, int G, uint64_t *twice_out,
                                   uint64_t *pairs_out, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* The target pass over the admitted tokens: paged 4-bit cache and attention.
+ * [PL] §2: one target pass checks the drafted tokens; [KB] Key Contributions:
+ * the scheduler prunes tokens from verification.  Between dspark_schedule and
+ * dspark_verify the target model runs over request b's last committed token
+ * and its ell[b] admitted draft tokens.  These calls keep that pass's state:
+ *   dspark_cache_plan       rows, positions, slots and pages for the round
+ *   dspark_qk_norm_rope     per layer: head norms, rotation, cache write
+ *   dspark_cache_attention  per layer: attention over the cache
+ *   dspark_cache_commit     after verification: keep the accepted tokens
+ *
+ * Cache: one array per layer, [n_pages, Hkv, R] bytes on a 16-byte boundary.
+ * A page holds P (16, 32, 64 or 128) tokens of one request; the record of a
+ * page and head is R = P * D * 9 / 8 bytes (D = 64 or 128):
+ *   K codes [D/32][P][16] | K scales [P][D/16] | V codes | V scales.
+ * Byte j of a 16-byte piece holds dims 2j (low nibble) and 2j + 1 of its
+ * 32-dim chunk as e2m1; a scale byte is the e4m3 scale of 16 dims; the value
+ * is code * scale * k_scale (v_scale).  The scales k_scale and v_scale belong
+ * to the layer, are positive and finite, and are 1 unless values lie outside
+ * about [2^-9, 2688].  The cache needs no initialisation.
+ * Slot of token t of a request: table[b, t / P] * P + t % P.
+ * The tokens of a round are packed by request: rows q_start[b] .. q_start[b+1],
+ * q_start[B] rows in all, in arrays sized for B * (G + 1).
+ * Every call takes a workspace for its status word (256 bytes are enough
+ * except for dspark_cache_attention) and may share it as above. */
+
+/* Bytes of one record, 0 for an unsupported page size or head dim. */
+size_t dspark_cache_record_bytes(int P, int D);
+
+/* Block tables, slots and positions of a round.
+ * Request b with ctx[b] >= 0 cached tokens takes n_b = ell[b] + 1 new ones at
+ * positions ctx[b] ..; ctx[b] < 0 is an empty seat (n_b = 0).  held[b] pages
+ * are in row b of the table; the pages it lacks come from the top of the free
+ * list (free_list[free_count - 1] downwards), request after request.  A
+ * request whose pages do not all fit (the list, or max_pages) gets none and
+ * takes only the tokens its own pages hold (DSPARK_DEV_CACHE_FULL; then
+ * q_start[b+1] - q_start[b] < ell[b] + 1).
+ * In and out: table [B, max_pages], held [B], free_count [1]; free_list
+ *          [n_pages] is read.
+ * Inputs:  ctx [B], ell [B] (clamped to [0, G], DSPARK_DEV_ELL_RANGE).
+ * Outputs: q_start_out [B+1]; kv_len_out [B] = ctx + n_b (0 for an empty
+ *          seat); slot_out and pos_out [B * (G+1)], -1 behind the last row.
+ * Limits:  B <= 4096, 0 <= G <= 2^20, B * (G+1) <= 2^24, n_pages * P < 2^31.
+ * Calling it again for the same lengths gives the same outputs and takes no
+ * further pages.  One launch. */
+dspark_status dspark_cache_plan(const int32_t *ctx, const int32_t *ell, int B, int G, int P, int max_pages,
+                                int n_pages, int32_t *table, int32_t *held, const int32_t *free_list,
+                                int32_t *free_count, void *ws, size_t ws_bytes, int32_t *q_start_out,
+                                int32_t *kv_len_out, int32_t *slot_out, int32_t *pos_out, void *stream);
+
+/* After verification: ctx_out[b] = ctx[b] + nout[b] (nout: dspark_verify's
+ * counts, at most the planned n_b), and the pages behind those tokens go back
+ * on the free list, so that committing nothing after a plan restores it.
+ * done [B] or NULL: a request with done[b] != 0 leaves (ctx_out[b] = -1, all
+ * its pages freed); an empty seat stays empty and frees what it holds.
+ * ctx_out may be ctx.  One launch. */
+dspark_status dspark_cache_commit(const int32_t *ctx, const int32_t *q_start, const int32_t *nout,
+                                  const int32_t *done, int B, int P, int max_pages, int n_pages, int32_t *table,
+                                  int32_t *held, int32_t *free_list, int32_t *free_count, void *ws, size_t ws_bytes,
+                                  int32_t *ctx_out, void *stream);
+
+/* Norm, rotation and cache write of a layer's projections, in one pass.
+ *   y = x / sqrt(mean(x^2) + eps) * w per query and key head (wq, wk [D]
+ *   dtype; NULL: y = x), then pairs (i, i + rot/2), or (2i, 2i + 1) with
+ *   interleaved != 0, of the first rot dims turn by pos[t] * inv_freq[i].
+ * Inputs:  q [T, Hq, D], k and v [T, Hkv, D] dtype, tokens q_stride (k_stride,
+ *          v_stride) elements apart, each token's heads dense, base and stride
+ *          on 16-byte boundaries; pos [T] int32; inv_freq [rot/2] f32 (both
+ *          unused for rot = 0); n_rows: device int32 (q_start + B) or NULL
+ *          for all T.  Rows from *n_rows on are left alone.
+ * Outputs: q_out [T, Hq, D], k_out [T, Hkv, D] dtype, dense; q_out may be q
+ *          and k_out may be k where those are dense.  k_out may be NULL when
+ *          cache is given.
+ * Cache:   NULL, or the layer's cache: y of the keys and v go to slot[t]
+ *          (negative: nowhere).  Two rows must not name one slot.  NaN is
+ *          stored as 0 and infinities as the largest value
+ *          (DSPARK_DEV_BAD_VALUE).
+ * Limits:  D = 64 or 128, rot a multiple of 32 up to D, Hq a multiple of Hkv,
+ *          Hq <= 1024, T <= 2^24.  fp32 inside, one rounding at the end. */
+dspark_status dspark_qk_norm_rope(const void *q, long long q_stride, const void *k, long long k_stride,
+                                  const void *v, long long v_stride, const void *wq, const void *wk, float eps,
+                                  const int32_t *pos, const float *inv_freq, int rot, int interleaved,
+                                  const int32_t *n_rows, int T, int Hq, int Hkv, int D, int dtype, void *q_out,
+                                  void *k_out, void *cache, const int32_t *slot, int P, int n_pages, float k_scale,
+                                  float v_scale, void *ws, size_t ws_bytes, void *stream);
+
+/* The cached keys and values of slot[0..T): k_out, v_out [T, Hkv, D] dtype
+ * (exact in bf16 for power-of-two k_scale, v_scale).  Rows with a negative
+ * slot are left alone. */
+dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, int Hkv, int D, int P, int n_pages,
+                                float k_scale, float v_scale, int dtype, void *k_out, void *v_out, void *ws,
+                                size_t ws_bytes, void *stream);
+
+/* Attention of the round's tokens over the cache.  Token j of request b has
+ * position p = kv_len[b] - n_b + j and sees keys max(0, p - window + 1) .. p
+ * (window = 0: all up to p), scores times `scale`; query head hq reads key
+ * head hq / (Hq / Hkv).  A token that sees no key gives zeros.  Rows from
+ * q_start[B] on are left alone.
+ * Inputs:  q [T, Hq, D] bf16, tokens q_stride elements apart as above; table
+ *          [B, max_pages], q_start [B+1], kv_len [B] as dspark_cache_plan
+ *          leaves them, after the round's keys were written.
+ * Outputs: out [T, Hq, D] bf16, dense.
+ * fp32 scores, maxima and sums; probabilities enter the second product in
+ * f16, keys, values and queries exactly.  Any n_b and any group Hq / Hkv.
+ * Deterministic.  Two launches.  bf16 only (DSPARK_ERR_UNSUPPORTED_DTYPE). */
+size_t dspark_cache_attention_workspace_size(int B, int Hq, int Hkv, int D);
+dspark_status dspark_cache_attention(const void *q, long long q_stride, const void *cache, const int32_t *table,
+                                     const int32_t *q_start, const int32_t *kv_len, int B, int T, int Hq, int Hkv,
+                                     int D, int P, int max_pages, int n_pages, float scale, float k_scale,
+                                     float v_scale, int window, int dtype, void *ws, size_t ws_bytes, void *out,
+                                     void *stream);
 
 /* Device status word of a workspace: dspark_get_device_status synchronises
  * `stream`, then copies the word to *status_out (0 = no data error since the

@@ -26,6 +26,7 @@ SCHED_TOPK = 4
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_DTYPE", 3: "WORKSPACE", 4: "CUDA", 5: "TIMEOUT"}
 DEV_TOKEN_RANGE, DEV_ELL_RANGE, DEV_BAD_TEMP, DEV_TIMEOUT, DEV_BAD_VALUE = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_CACHE_FULL, DEV_PAGE_RANGE, DEV_LENGTH_RANGE = 0x20, 0x40, 0x80
 
 EXPORTS = ("dspark_version", "dspark_draft_workspace_size", "dspark_draft_markov", "dspark_confidence",
            "dspark_schedule_workspace_size", "dspark_schedule", "dspark_verify_workspace_size",
@@ -33,7 +34,9 @@ EXPORTS = ("dspark_version", "dspark_draft_workspace_size", "dspark_draft_markov
            "dspark_draft_noalloc_max_scratch", "dspark_draft_markov_noalloc", "dspark_schedule_threshold",
            "dspark_sts_workspace_size", "dspark_sts_fit", "dspark_survival_auc", "dspark_schedule_topk",
            "dspark_draft_noalloc_device_status", "dspark_draft_rnn", "dspark_verify_rnn", "dspark_get_near_ties",
-           "dspark_exp2_fma", "dspark_gather_admitted_targets")
+           "dspark_exp2_fma", "dspark_gather_admitted_targets", "dspark_cache_record_bytes", "dspark_cache_plan",
+           "dspark_cache_commit", "dspark_qk_norm_rope", "dspark_cache_read",
+           "dspark_cache_attention_workspace_size", "dspark_cache_attention")
 
 
 class DsparkError(RuntimeError):
@@ -44,6 +47,7 @@ class DsparkError(RuntimeError):
 
 _lib = None
 _vp, _i, _f, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_double
+_ll = ctypes.c_longlong
 
 
 def load() -> ctypes.CDLL:
@@ -100,6 +104,22 @@ def load() -> ctypes.CDLL:
     lib.dspark_survival_auc.argtypes = [_vp, _vp, _i, _i, _vp, _vp, _vp]
     lib.dspark_gather_admitted_targets.restype = _i
     lib.dspark_gather_admitted_targets.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _vp]
+    lib.dspark_cache_record_bytes.restype = _sz
+    lib.dspark_cache_record_bytes.argtypes = [_i] * 2
+    lib.dspark_cache_plan.restype = _i
+    lib.dspark_cache_plan.argtypes = [_vp] * 2 + [_i] * 5 + [_vp] * 5 + [_sz] + [_vp] * 5
+    lib.dspark_cache_commit.restype = _i
+    lib.dspark_cache_commit.argtypes = [_vp] * 4 + [_i] * 4 + [_vp] * 5 + [_sz] + [_vp] * 2
+    lib.dspark_qk_norm_rope.restype = _i
+    lib.dspark_qk_norm_rope.argtypes = ([_vp, _ll] * 3 + [_vp] * 2 + [_f] + [_vp] * 2 + [_i] * 2 + [_vp] + [_i] * 5 +
+                                        [_vp] * 4 + [_i] * 2 + [_f] * 2 + [_vp, _sz, _vp])
+    lib.dspark_cache_read.restype = _i
+    lib.dspark_cache_read.argtypes = [_vp] * 2 + [_i] * 5 + [_f] * 2 + [_i] + [_vp] * 3 + [_sz, _vp]
+    lib.dspark_cache_attention_workspace_size.restype = _sz
+    lib.dspark_cache_attention_workspace_size.argtypes = [_i] * 4
+    lib.dspark_cache_attention.restype = _i
+    lib.dspark_cache_attention.argtypes = ([_vp, _ll] + [_vp] * 4 + [_i] * 8 + [_f] * 3 + [_i] * 2 +
+                                           [_vp, _sz] + [_vp] * 2)
     _lib = lib
     return lib
 
@@ -288,6 +308,168 @@ def dspark_gather_admitted_targets(Tlog_host, Tlog_dev, ell, stream=None):
     B, G1, V = Tlog_dev.shape
     _call("dspark_gather_admitted_targets", ctypes.c_void_p(Tlog_host.data_ptr()), _ptr(Tlog_dev), _ptr(ell), B,
           G1 - 1, V, _dtype(Tlog_dev), _stream(stream))
+
+
+def _rows(t, what):
+    """(pointer, token stride) of a [T, H, D] device tensor whose heads are dense; the tokens may lie apart (a
+    slice of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError("libdspark takes device tensors")
+    T, H, D = t.shape
+    s = t.stride()
+    if s[2] != 1 or (H > 1 and s[1] != D):
+        raise ValueError(f"{what}: the heads of a token must be dense")
+    return ctypes.c_void_p(t.data_ptr()), (s[0] if T > 1 else max(s[0], H * D))
+
+
+def _ints(n, what, *tensors):
+    for t in tensors:
+        if t.dtype != torch.int32 or t.numel() < n:
+            raise ValueError(f"{what}: int32 tensors of at least {n} elements, got {t.dtype} of {t.numel()}")
+
+
+def _launch(fn, t, stream, *args):
+    """Call `fn` with the stream of t's device appended, on that device (which need not be the current one)."""
+    if t.device.index == torch.cuda.current_device():
+        _call(fn, *args, _stream(stream))
+    else:
+        with torch.cuda.device(t.device):
+            _call(fn, *args, _stream(stream))
+
+
+def _same_device(*tensors):
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def _cache_dims(cache, page, D):
+    """(n_pages, Hkv) of a cache tensor [n_pages, Hkv, record bytes]."""
+    need = dspark_cache_record_bytes(page, D)
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or need == 0 or cache.shape[2] != need:
+        raise ValueError(f"cache: uint8 [n_pages, Hkv, {need}] for pages of {page} tokens and heads of {D}, got "
+                         f"{cache.dtype} {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1]
+
+
+def dspark_cache_record_bytes(page, D) -> int:
+    """Bytes of one (page, head) record of the 4-bit cache; 0 for an unsupported page size or head dim."""
+    return int(load().dspark_cache_record_bytes(page, D))
+
+
+def dspark_cache_plan(ctx, ell, G, table, held, free_list, free_count, page, ws, q_start_out, kv_len_out, slot_out,
+                      pos_out, stream=None):
+    """Rows, slots, positions and pages of a round from the cached lengths
+    ctx [B] and admitted lengths ell [B]; table [B, max_pages], held [B] and
+    free_count [1] are updated, free_list [n_pages] is read.  slot_out and
+    pos_out hold B * (G + 1) entries, -1 behind the last row."""
+    B, max_pages = table.shape
+    _ints(B, "ctx, ell, held, kv_len_out", ctx, ell, held, kv_len_out)
+    _ints(B + 1, "q_start_out", q_start_out)
+    _ints(B * (G + 1), "slot_out, pos_out", slot_out, pos_out)
+    _ints(1, "table, free_list, free_count", table, free_list, free_count)
+    _same_device(ctx, ell, table, held, free_list, free_count, ws, q_start_out, kv_len_out, slot_out, pos_out)
+    _launch("dspark_cache_plan", table, stream, _ptr(ctx), _ptr(ell), B, int(G), int(page), max_pages,
+            free_list.numel(), _ptr(table), _ptr(held), _ptr(free_list), _ptr(free_count), _ptr(ws),
+            ws.numel() * ws.element_size(), _ptr(q_start_out), _ptr(kv_len_out), _ptr(slot_out), _ptr(pos_out))
+
+
+def dspark_cache_commit(ctx, q_start, nout, done, table, held, free_list, free_count, page, ws, ctx_out,
+                        stream=None):
+    """After verification: ctx_out = ctx + nout (-1 where done [B], or None,
+    is set), and the pages behind those tokens go back on the free list.
+    ctx_out may be ctx."""
+    B, max_pages = table.shape
+    _ints(B, "ctx, nout, held, ctx_out", ctx, nout, held, ctx_out)
+    _ints(B + 1, "q_start", q_start)
+    _ints(1, "table, free_list, free_count", table, free_list, free_count)
+    if done is not None:
+        _ints(B, "done", done)
+    _same_device(ctx, q_start, nout, done, table, held, free_list, free_count, ws, ctx_out)
+    _launch("dspark_cache_commit", table, stream, _ptr(ctx), _ptr(q_start), _ptr(nout), _ptr(done), B, int(page),
+            max_pages, free_list.numel(), _ptr(table), _ptr(held), _ptr(free_list), _ptr(free_count), _ptr(ws),
+            ws.numel() * ws.element_size(), _ptr(ctx_out))
+
+
+def dspark_qk_norm_rope(q, k, wq, wk, eps, pos, inv_freq, interleaved, n_rows, q_out, k_out, ws, v=None, cache=None,
+                        slot=None, page=64, k_scale=1.0, v_scale=1.0, stream=None):
+    """Head norms, rotation and (with cache, v and slot) the write of keys and
+    values into the 4-bit cache.  q [T, Hq, D], k and v [T, Hkv, D] may be
+    slices of one projection; inv_freq [rot/2] f32 (None: no rotation); wq, wk
+    [D] or None (no norm); n_rows: device int32 tensor or None."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D) or q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
+        raise ValueError("q, k, q_out and k_out differ in tokens, heads or dims")
+    for t in (k, v, wq, wk, q_out, k_out):
+        if t is not None and t.dtype != q.dtype:
+            raise ValueError(f"one dtype for q, k, v, the weights and the outputs: {t.dtype} and {q.dtype}")
+    for w in (wq, wk):
+        if w is not None and w.numel() != D:
+            raise ValueError(f"norm weights have {D} elements")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot:
+        if inv_freq.dtype != torch.float32:
+            raise ValueError("inv_freq is float32")
+        _ints(T, "pos", pos)
+    if n_rows is not None:
+        _ints(1, "n_rows", n_rows)
+    n_pages = 0
+    if cache is not None:
+        n_pages, heads = _cache_dims(cache, page, D)
+        if v is None or slot is None or v.shape != k.shape or heads != Hkv:
+            raise ValueError("a cache write needs v like k, slot, and a cache of k's heads")
+        _ints(T, "slot", slot)
+    _same_device(q, k, v, wq, wk, pos if rot else None, inv_freq, n_rows, q_out, k_out, ws, cache, slot)
+    qp, qs = _rows(q, "q")
+    kp, ks = _rows(k, "k")
+    vp, vs = (None, 0) if v is None else _rows(v, "v")
+    _launch("dspark_qk_norm_rope", q, stream, qp, qs, kp, ks, vp, vs, _ptr(wq), _ptr(wk), float(eps),
+            _ptr(pos) if rot else None, _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), _ptr(n_rows),
+            T, Hq, Hkv, D, _dtype(q), _ptr(q_out), _ptr(k_out), _ptr(cache), _ptr(slot), int(page), n_pages,
+            float(k_scale), float(v_scale), _ptr(ws), ws.numel() * ws.element_size())
+
+
+def dspark_cache_read(cache, slot, page, k_out, v_out, ws, k_scale=1.0, v_scale=1.0, stream=None):
+    """Keys and values of the cached tokens slot [T] -> k_out, v_out
+    [T, Hkv, D]; rows with a negative slot are left alone."""
+    T, Hkv, D = k_out.shape
+    n_pages, heads = _cache_dims(cache, page, D)
+    if v_out.shape != k_out.shape or v_out.dtype != k_out.dtype or heads != Hkv:
+        raise ValueError("k_out, v_out and the cache differ in heads, dims or dtype")
+    _ints(T, "slot", slot)
+    _same_device(cache, slot, k_out, v_out, ws)
+    _launch("dspark_cache_read", cache, stream, _ptr(cache), _ptr(slot), T, Hkv, D, int(page), n_pages,
+            float(k_scale), float(v_scale), _dtype(k_out), _ptr(k_out), _ptr(v_out), _ptr(ws),
+            ws.numel() * ws.element_size())
+
+
+def dspark_cache_attention_workspace_size(B, Hq, Hkv, D) -> int:
+    return int(load().dspark_cache_attention_workspace_size(B, Hq, Hkv, D))
+
+
+def dspark_cache_attention(q, cache, table, q_start, kv_len, page, scale, window, ws, out, k_scale=1.0, v_scale=1.0,
+                           stream=None):
+    """Attention of the round's rows q [T, Hq, D] (bf16) over the 4-bit cache:
+    causal inside each request's block, the last `window` keys only when
+    window > 0; table, q_start and kv_len as dspark_cache_plan leaves them."""
+    T, Hq, D = q.shape
+    B, max_pages = table.shape
+    n_pages, Hkv = _cache_dims(cache, page, D)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out differ in shape or dtype")
+    _ints(B + 1, "q_start", q_start)
+    _ints(B, "kv_len", kv_len)
+    _ints(1, "table", table)
+    _same_device(q, cache, table, q_start, kv_len, ws, out)
+    qp, qs = _rows(q, "q")
+    _launch("dspark_cache_attention", q, stream, qp, qs, _ptr(cache), _ptr(table), _ptr(q_start), _ptr(kv_len), B, T,
+            Hq, Hkv, D, int(page), max_pages, n_pages, float(scale), float(k_scale), float(v_scale), int(window),
+            _dtype(q), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out))
 
 
 def dspark_exp2_fma(x, y, stream=None):

@@ -1,0 +1,751 @@
+// cache_attention.cu -- attention of the target pass over the paged 4-bit
+// cache (tcgen05 / TMEM / bulk copies).
+//
+// For query row r (token j of request b, head hq; its key head h = hq / group)
+// at position p_r = kv_len[b] - n_b + j, over the keys i it may see
+// (max(0, p_r - window + 1) <= i <= p_r):
+//   x_i = qk_mul * <q_r, k_i>,  o_r = sum_i 2^(x_i - m) v_i / sum_i 2^(x_i - m).
+//
+// All rows of one request and key head (n_b * group, in blocks of 64) share
+// one pass over its keys: an item.  Items are cut into tiles of 128 keys, the
+// tiles of all items are laid end to end, and every CTA takes an equal run of
+// them, so ragged lengths and single long requests load the machine evenly.
+// An item that a CTA does not finish leaves (m, sum, o) in the workspace, and
+// a second kernel joins its parts in a fixed order.
+//
+// Keys are the M = 128 side of both products, so a tile costs little more for
+// one query row than for 64:
+//   S^T [keys x rows] = K Q^T      A = K in TMEM, B = Q in shared memory
+//   O^T [D x rows]   += V^T P^T    A = V in shared memory, B = P
+//   L   [.. x rows]  += 1 P^T      A = ones in TMEM: the softmax sums, of the
+//                                  rounded P that the products use
+// Roles of the 14 warps (one CTA per SM, 512 TMEM columns):
+//   warps 0-3    keys: a thread turns one token's codes into f16 in its TMEM lane
+//   warps 4-7    values: one token's codes into f16 in shared memory (D-major operand)
+//   warps 8-11   softmax: a thread owns one key of the tile, all rows; queries; results
+//   warp 12      producer: page table, one bulk copy per page record
+//   warp 13      MMA issuer
+// P is exp2 of the scaled score minus a running maximum that is only raised
+// (and O, L rescaled) when a score passes it by more than 8, so P <= 256 and
+// f16 keeps its 11 bits; K, V and Q (scaled by a power of two per row) are
+// exact in f16, so P's rounding is the only one before the output's.
+// Every wait is bounded: on expiry the roles run on without waiting, nothing
+// more is copied or multiplied, and the status word says so.
+#include "cache.cuh"
+#include "tc.cuh"
+
+namespace dspark {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;        // keys per tile
+constexpr int kRows = 64;         // query rows per item
+constexpr int kThreads = 448;
+constexpr int kMaxCtas = 160;
+constexpr long long kWaitBudget = 4000000000LL;
+constexpr float kRaise = 8.f;     // log2 room above the running maximum
+constexpr int kDescInts = 8;      // rem, q0, r0, nr, h, quota
+
+// TMEM columns.
+constexpr int kColK = 0, kColS = 128, kColO = 256, kColL = 320, kColOne = 384;
+
+template <int D>
+struct Lay {
+    static constexpr int kRec = kTile * D / 8 * 9;       // bytes of one tile's records
+    static constexpr int kVBytes = kTile * D * 2;
+    static constexpr int kPBytes = kTile * kRows * 2;
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int v = 0;
+    static constexpr int p = v + 2 * kVBytes;
+    static constexpr int q = p + 2 * kPBytes;
+    static constexpr int raw = q + kQBytes;
+    static constexpr int misc = raw + kStages * kRec;
+};
+
+struct Misc {
+    float2 row[kRows];       // (multiplier of the raw score, running maximum)
+    int2 lim[kRows];         // visible keys [x, y)
+    int orow[kRows];         // output row (token * Hq + head)
+    float fac[kRows];
+    float wmax[4][kRows];
+    uint64_t raw_full[8], raw_empty[8];
+    uint64_t k_full[2], s_full[2], v_full[2], p_full[2], pv_done[2], q_full, drain;
+    uint32_t tmem;
+    int abort;
+    int scan[16];
+};
+
+struct Req {
+    int q0, n, L;
+};
+
+__device__ __forceinline__ Req load_req(const AttnArgs &a, int b) {
+    Req r;
+    const int s0 = min(max(__ldg(a.q_start + b), 0), a.T), s1 = min(max(__ldg(a.q_start + b + 1), s0), a.T);
+    r.q0 = s0;
+    r.n = s1 - s0;
+    r.L = min(max(__ldg(a.kv_len + b), 0), a.max_pages * a.P);
+    return r;
+}
+
+// Row block rb of a request: rows [r0, r0 + nr), keys [base, hi) in tiles.
+struct Block {
+    int r0, nr, base, hi, nt;
+};
+__device__ __forceinline__ Block row_block(const AttnArgs &a, const Req &q, int rb) {
+    Block k;
+    k.r0 = rb * kRows;
+    k.nr = min(kRows, q.n * a.group - k.r0);
+    const int jf = k.r0 / a.group, jl = (k.r0 + k.nr - 1) / a.group;
+    k.hi = max(0, q.L - q.n + jl + 1);
+    const int lo = a.window > 0 ? max(0, q.L - q.n + jf - a.window + 1) : 0;
+    k.base = lo / a.P * a.P;
+    k.nt = max(1, (k.hi - k.base + kTile - 1) / kTile);   // a row block without keys still writes zeros
+    return k;
+}
+
+// This CTA's run of tiles, piece by piece (a piece: consecutive tiles of one item).
+struct Walk {
+    const AttnArgs &a;
+    int left;                // tiles left in the run
+    int b, rb, h, t0, t1;
+    Req q;
+    Block k;
+    __device__ __forceinline__ Walk(const AttnArgs &args, const int *prefix, int w0, int w1) : a(args) {
+        left = w1 - w0;
+        int lo = 0, hi = a.B;                // the request holding tile w0: prefix[b] <= w0 < prefix[b + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= w0) lo = mid; else hi = mid;
+        }
+        b = lo;
+        q = load_req(a, b);
+        int off = w0 - prefix[b];
+        for (rb = 0;; ++rb) {
+            k = row_block(a, q, rb);
+            if (off < k.nt * a.Hkv) break;
+            off -= k.nt * a.Hkv;
+        }
+        h = off / k.nt;
+        t0 = off - h * k.nt;
+        t1 = min(k.nt, t0 + left);
+    }
+    __device__ __forceinline__ bool next() {   // false: the run is done
+        left -= t1 - t0;
+        if (left <= 0) return false;
+        if (++h == a.Hkv) {
+            h = 0;
+            if ((rb + 1) * kRows < q.n * a.group) {
+                ++rb;
+            } else {
+                rb = 0;
+                do q = load_req(a, ++b); while (q.n == 0 && b + 1 < a.B);
+            }
+            k = row_block(a, q, rb);
+        }
+        t0 = 0;
+        t1 = min(k.nt, left);
+        return true;
+    }
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float warp_max_f32(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Bounded wait of a whole warp (converged again afterwards).  A try may sleep
+// for some microseconds, so a budget shorter than that is polled.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
+    if (budget >= 1000000) {
+        mbar_wait_bounded(bar, parity, abort, budget);
+    } else {
+        const long long t0 = clock64();
+        for (;;) {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity)
+                : "memory");
+            if (ok || *abort) break;
+            if (clock64() - t0 > budget) {
+                *abort = 1;
+                break;
+            }
+        }
+    }
+    __syncwarp();
+}
+// The 128 softmax threads.
+__device__ __forceinline__ void soft_sync() {
+    __syncwarp();
+    asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+}
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.aligned.pred p, 1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+// 128-byte swizzled operand whose rows (128 bytes) run along K (the row
+// dimension is contiguous): 8-row groups 1024 bytes apart, 64-element blocks
+// of the row dimension `lbo` bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
+           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16 with f16 operands and fp32 sums, M = 128.
+__device__ __forceinline__ uint32_t idesc_f16(int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// 16 bytes of codes and two scales -> 16 f16x2.
+__device__ __forceinline__ void unpack32(const uint4 c, uint32_t s0, uint32_t s1, uint32_t (&r)[16]) {
+    e2m1x8_to_f16(c.x, r[0], r[1], r[2], r[3]);
+    e2m1x8_to_f16(c.y, r[4], r[5], r[6], r[7]);
+    e2m1x8_to_f16(c.z, r[8], r[9], r[10], r[11]);
+    e2m1x8_to_f16(c.w, r[12], r[13], r[14], r[15]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = mul_f16x2(r[i], s0);
+#pragma unroll
+    for (int i = 8; i < 16; ++i) r[i] = mul_f16x2(r[i], s1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const AttnArgs a) {
+    using Y = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    Misc &ms = *reinterpret_cast<Misc *>(sm + Y::misc);
+    int *prefix = reinterpret_cast<int *>(sm + Y::misc + (sizeof(Misc) + 15) / 16 * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = Y::kStages;
+
+    // Tiles of every request, and their prefix: thread t sums a run of requests.
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int sum = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        const Req q = load_req(a, b);
+        bad |= __ldg(a.kv_len + b) != q.L || __ldg(a.q_start + b) != q.q0 || __ldg(a.q_start + b + 1) != q.q0 + q.n;
+        int t = 0;
+        for (int rb = 0; rb * kRows < q.n * a.group; ++rb) t += row_block(a, q, rb).nt;
+        prefix[b] = sum;
+        sum += t * a.Hkv;
+    }
+    if (bad && blockIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_LENGTH_RANGE);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) ms.scan[warp] = inc;
+    if (tid == 0) {
+        ms.abort = 0;
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&ms.raw_full[i], 1);
+            mbar_init(&ms.raw_empty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.k_full[i], 4);
+            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.v_full[i], 4);
+            mbar_init(&ms.p_full[i], 4);
+            mbar_init(&ms.pv_done[i], 1);
+        }
+        mbar_init(&ms.q_full, 4);
+        mbar_init(&ms.drain, 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    int before = inc - sum, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += ms.scan[w];
+        total += ms.scan[w];
+    }
+    for (int b = b0; b < b1; ++b) prefix[b] += before;
+    const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int w0 = min(total, (int)blockIdx.x * quota), w1 = min(total, w0 + quota);
+    if (w0 >= w1) {   // the whole CTA: no work, nothing left unfinished
+        if (tid == 0) a.desc[blockIdx.x * kDescInts] = 0;
+        return;
+    }
+    if (warp == 0) {
+        tmem_alloc(&ms.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ms.tmem;
+    volatile int *abort = &ms.abort;
+    Walk wk(a, prefix, w0, w1);
+    int g = 0;   // tiles done by this role
+    int issued = 0;
+
+    if (warp < 4) {
+        // ---------------------------------------------------------- keys
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const int key = tid, R = record_bytes(a.P, D);
+        const int koff = key / a.P * R + key % a.P * 16;
+        const int soff = key / a.P * R + half_scales_off(a.P, D) + key % a.P * (D / 16);
+        {
+            uint32_t one[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) one[i] = 0x3c003c00u;
+            tmem_st16(tm + lane_base + kColOne, one);
+        }
+        do {
+            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+                const int st = g % S, bb = g & 1;
+                wait(&ms.raw_full[st], (g / S) & 1, abort, a.budget);
+                wait(&ms.s_full[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
+                tc_fence_after();
+                const uint8_t *raw = sm + Y::raw + st * Y::kRec;
+                uint32_t sc[D / 64];
+                if (D == 128) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(raw + soff);
+                    sc[0] = v.x;
+                    sc[D / 64 - 1] = v.y;
+                } else {
+                    sc[0] = *reinterpret_cast<const uint32_t *>(raw + soff);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    const uint4 codes = *reinterpret_cast<const uint4 *>(raw + koff + c * a.P * 16);
+                    uint32_t r[16];
+                    const uint32_t s0 = c & 1 ? scale_f16x2<2>(sc[c / 2]) : scale_f16x2<0>(sc[c / 2]);
+                    const uint32_t s1 = c & 1 ? scale_f16x2<3>(sc[c / 2]) : scale_f16x2<1>(sc[c / 2]);
+                    unpack32(codes, s0, s1, r);
+                    tmem_st16(tm + lane_base + kColK + bb * 64 + c * 16, r);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ms.k_full[bb]);
+                    mbar_arrive(&ms.raw_empty[st]);
+                }
+            }
+        } while (wk.next());
+    } else if (warp < 8) {
+        // -------------------------------------------------------- values
+        const int key = tid - 128, R = record_bytes(a.P, D);
+        const int half = half_bytes(a.P, D);
+        const int voff = key / a.P * R + half + key % a.P * 16;
+        const int soff = key / a.P * R + half + half_scales_off(a.P, D) + key % a.P * (D / 16);
+        do {
+            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+                const int st = g % S, bb = g & 1;
+                wait(&ms.raw_full[st], (g / S) & 1, abort, a.budget);
+                wait(&ms.pv_done[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
+                const uint8_t *raw = sm + Y::raw + st * Y::kRec;
+                uint8_t *vrow = sm + Y::v + bb * Y::kVBytes + key * 128;
+                uint32_t sc[D / 64];
+                if (D == 128) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(raw + soff);
+                    sc[0] = v.x;
+                    sc[D / 64 - 1] = v.y;
+                } else {
+                    sc[0] = *reinterpret_cast<const uint32_t *>(raw + soff);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    const uint4 codes = *reinterpret_cast<const uint4 *>(raw + voff + c * a.P * 16);
+                    uint32_t r[16];
+                    const uint32_t s0 = c & 1 ? scale_f16x2<2>(sc[c / 2]) : scale_f16x2<0>(sc[c / 2]);
+                    const uint32_t s1 = c & 1 ? scale_f16x2<3>(sc[c / 2]) : scale_f16x2<1>(sc[c / 2]);
+                    unpack32(codes, s0, s1, r);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int piece = ((c & 1) * 4 + u) ^ (key & 7);
+                        *reinterpret_cast<uint4 *>(vrow + (c / 2) * (kTile * 128) + piece * 16) =
+                            make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ms.v_full[bb]);
+                    mbar_arrive(&ms.raw_empty[st]);
+                }
+            }
+        } while (wk.next());
+    } else if (warp < 12) {
+        // ------------------------------------------------------- softmax
+        const int key = tid - 256, sw = warp - 8;
+        const uint32_t lane_base = (uint32_t)(sw * 32) << 16;
+        if (key == 0) a.desc[blockIdx.x * kDescInts] = 0;
+        do {
+            const int nr = wk.k.nr, N = (nr + 15) / 16 * 16;
+            // Queries: D / 8 lanes a row, scaled by a power of two so that f16 holds them exactly.
+            {
+                constexpr int kLanes = D / 8, kPass = 128 / kLanes;
+                const int piece = key % kLanes;
+                for (int r = key / kLanes; r < N; r += kPass) {
+                    const bool live = r < nr;
+                    const int gr = wk.k.r0 + r, j = gr / a.group, hd = wk.h * a.group + gr % a.group;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (live)
+                        w = *reinterpret_cast<const uint4 *>(a.q + (long long)(wk.q.q0 + j) * a.q_stride + hd * D +
+                                                             piece * 8);
+                    float f[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y),
+                                  bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
+                    float mx = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[i]));
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // 2^e * max in [2^14, 2^15); e within fp32's exponents.
+                    const int ex = (int)(__float_as_uint(mx) >> 23) - 127;
+                    const int e = (mx > 0.f && ex < 128) ? min(14 - ex, 100) : 0;
+                    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    uint32_t hh[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2 x = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+                        hh[i] = *reinterpret_cast<const uint32_t *>(&x);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + Y::q + (piece / 8) * (kRows * 128) + r * 128 +
+                                               (((piece & 7) ^ (r & 7)) * 16)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                    if (piece == 0) {
+                        const int pos = wk.q.L - wk.q.n + j;
+                        ms.row[r] = live ? make_float2(a.qk_mul * down, -INFINITY) : make_float2(0.f, 0.f);
+                        ms.lim[r] = live ? make_int2(a.window > 0 ? max(0, pos - a.window + 1) : 0, pos + 1)
+                                         : make_int2(0, 0);
+                        ms.orow[r] = (wk.q.q0 + j) * a.Hq + hd;
+                    }
+                }
+                fence_proxy_async_smem();
+                soft_sync();
+                if (lane == 0) mbar_arrive(&ms.q_full);
+            }
+            // Tiles that every row sees whole need no mask.
+            const int all_hi = ms.lim[0].y, all_lo = ms.lim[nr - 1].x;
+            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+                const int bb = g & 1;
+                const int kpos = wk.k.base + t * kTile;
+                const bool masked = kpos + kTile > all_hi || kpos < all_lo;
+                const int me = kpos + key;
+                uint8_t *prow = sm + Y::p + bb * Y::kPBytes + key * 128;
+                const uint32_t ts = tm + lane_base + kColS + bb * 64;
+                wait(&ms.s_full[bb], (g >> 1) & 1, abort, a.budget);
+                wait(&ms.pv_done[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
+                tc_fence_after();
+                bool raise = t == wk.t0;
+                for (int pass = 0;; ++pass) {
+                    if (raise) {
+                        // New maxima over the tile: a warp's 32 keys, then the four warps.
+                        for (int c = 0; c < N; c += 16) {
+                            float s[16];
+                            tmem_ld16(ts + c, s);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float x = s[i] * ms.row[c + i].x;
+                                if (masked) {
+                                    const int2 l = ms.lim[c + i];
+                                    if (me < l.x || me >= l.y) x = -INFINITY;
+                                }
+                                x = warp_max_f32(x);
+                                if (lane == i) ms.wmax[sw][c + i] = x;
+                            }
+                        }
+                        soft_sync();
+                        if (key < N) {
+                            const float old = ms.row[key].y;
+                            const float nm = fmaxf(fmaxf(fmaxf(ms.wmax[0][key], ms.wmax[1][key]),
+                                                         fmaxf(ms.wmax[2][key], ms.wmax[3][key])), old);
+                            ms.fac[key] = nm == old ? 1.f : fast_exp2(old - nm);
+                            ms.row[key].y = nm;
+                        }
+                        soft_sync();
+                        if (t > wk.t0) {
+                            wait(&ms.pv_done[bb ^ 1], ((g - 1) >> 1) & 1, abort, a.budget);
+                            tc_fence_after();
+                            for (int c = 0; c < N; c += 16) {
+#pragma unroll
+                                for (int w = 0; w < 2; ++w) {
+                                    const uint32_t at = tm + lane_base + (w ? kColL : kColO) + c;
+                                    float o[16];
+                                    uint32_t u[16];
+                                    tmem_ld16(at, o);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * ms.fac[c + i]);
+                                    tmem_st16(at, u);
+                                }
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    float top = -INFINITY;
+                    for (int c = 0; c < N; c += 16) {
+                        float s[16];
+                        tmem_ld16(ts + c, s);
+                        uint32_t ph[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 rm = *reinterpret_cast<const float4 *>(&ms.row[c + i]);
+                            float x0 = fmaf(s[i], rm.x, -rm.y), x1 = fmaf(s[i + 1], rm.z, -rm.w);
+                            if (masked) {
+                                const int4 l = *reinterpret_cast<const int4 *>(&ms.lim[c + i]);
+                                if (me < l.x || me >= l.y) x0 = -INFINITY;
+                                if (me < l.z || me >= l.w) x1 = -INFINITY;
+                            }
+                            top = max3(top, x0, x1);
+                            const __half2 h2 = __floats2half2_rn(fast_exp2(x0), fast_exp2(x1));
+                            ph[i / 2] = *reinterpret_cast<const uint32_t *>(&h2);
+                        }
+                        *reinterpret_cast<uint4 *>(prow + (((c / 8) ^ (key & 7)) * 16)) =
+                            make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                        *reinterpret_cast<uint4 *>(prow + (((c / 8 + 1) ^ (key & 7)) * 16)) =
+                            make_uint4(ph[4], ph[5], ph[6], ph[7]);
+                    }
+                    if (raise) break;                       // at most one raise a tile
+                    raise = soft_any(top > kRaise);
+                    if (!raise) break;
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.p_full[bb]);
+            }
+            // The piece's result: this thread's dim of every row.
+            wait(&ms.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, a.budget);
+            tc_fence_after();
+            const bool whole = wk.t0 == 0 && wk.t1 == wk.k.nt;
+            const int slot = 2 * blockIdx.x + (wk.t0 == 0 ? 1 : 0);
+            for (int c = 0; c < N; c += 16) {
+                float o[16], l[16];
+                tmem_ld16(tm + lane_base + kColO + c, o);
+                tmem_ld16(tm + lane_base + kColL + c, l);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = c + i;
+                    if (r < nr) {
+                        if (whole) {
+                            const float y = l[i] == 0.f ? 0.f : o[i] / l[i] * a.v_mul;
+                            if (key < D) a.out[(long long)ms.orow[r] * D + key] = __float2bfloat16_rn(y);
+                        } else {
+                            if (key < D) a.part_o[((size_t)slot * kRows + r) * D + key] = o[i];
+                            if (key == 0) a.part_ml[slot * kRows + r] = make_float2(ms.row[r].y, l[i]);
+                        }
+                    }
+                }
+            }
+            if (!whole && wk.t0 == 0 && key == 0) {
+                int32_t *d = a.desc + blockIdx.x * kDescInts;
+                d[1] = wk.q.q0;
+                d[2] = wk.k.r0;
+                d[3] = nr;
+                d[4] = wk.h;
+                d[5] = quota;
+                d[0] = wk.k.nt - wk.t1;
+            }
+            tc_fence_before();
+            soft_sync();   // before the rows' state is rewritten
+        } while (wk.next());
+    } else if (warp == 12) {
+        // ------------------------------------------------------ producer
+        const uint64_t pol = policy_evict_first();
+        const int R = record_bytes(a.P, D), ppt = kTile / a.P;
+        do {
+            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+                const int st = g % S;
+                const int key0 = wk.k.base + t * kTile;
+                const int np = min(ppt, max(0, (wk.k.hi - key0 + a.P - 1) / a.P));
+                int page = 0;
+                if (lane < np) {
+                    page = __ldg(a.table + (long long)wk.b * a.max_pages + key0 / a.P + lane);
+                    if (page < 0 || page >= a.n_pages) {
+                        flag_status(a.hdr, DSPARK_DEV_PAGE_RANGE);
+                        page = 0;
+                    }
+                }
+                wait(&ms.raw_empty[st], ((g / S) & 1) ^ 1, abort, a.budget);
+                const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
+                if (go) {
+                    if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], (uint32_t)(np * R));
+                    __syncwarp();
+                    if (lane < np)
+                        bulk_load(sm + Y::raw + st * Y::kRec + lane * R,
+                                  a.cache + ((size_t)page * a.Hkv + wk.h) * R, (uint32_t)R, &ms.raw_full[st], pol);
+                    issued = g + 1;
+                }
+            }
+        } while (wk.next());
+    } else {
+        // ----------------------------------------------------------- MMA
+        int piece = 0;
+        const uint32_t qb = smem_u32(sm + Y::q);
+        do {
+            const int N = (wk.k.nr + 15) / 16 * 16;
+            const uint32_t id_s = idesc_f16(N, false, false), id_o = idesc_f16(N, true, true),
+                           id_l = idesc_f16(N, false, true);
+            wait(&ms.q_full, piece & 1, abort, a.budget);
+            ++piece;
+            const int g_end = g + (wk.t1 - wk.t0);
+            auto scores = [&](int gg) {
+                const int bb = gg & 1;
+                wait(&ms.k_full[bb], (gg >> 1) & 1, abort, a.budget);
+                tc_fence_after();
+                const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
+                if (go && elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_bf16_ts(tm + kColS + bb * 64, tm + kColK + bb * 64 + kk * 8,
+                                    sw128_desc(qb + (kk / 4) * (kRows * 128) + (kk & 3) * 32), id_s, kk > 0);
+                    mma_commit(&ms.s_full[bb]);
+                }
+                __syncwarp();
+            };
+            scores(g);
+            for (bool first = true; g < g_end; ++g, first = false) {
+                if (g + 1 < g_end) scores(g + 1);
+                const int bb = g & 1;
+                wait(&ms.v_full[bb], (g >> 1) & 1, abort, a.budget);
+                wait(&ms.p_full[bb], (g >> 1) & 1, abort, a.budget);
+                tc_fence_after();
+                const uint32_t vb = smem_u32(sm + Y::v + bb * Y::kVBytes), pb = smem_u32(sm + Y::p + bb * Y::kPBytes);
+                const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
+                if (go && elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk) {
+                        const uint64_t pd = sw128_desc_mn(pb + kk * 2048, 0);
+                        const uint32_t acc = !first || kk > 0;
+                        // D = 64: the second 64 rows of the operand repeat the first (their lanes are not read).
+                        mma_bf16(tm + kColO, sw128_desc_mn(vb + kk * 2048, D == 128 ? kTile * 128 : 0), pd, id_o, acc);
+                        mma_bf16_ts(tm + kColL, tm + kColOne, pd, id_l, acc);
+                    }
+                    mma_commit(&ms.pv_done[bb]);
+                }
+                __syncwarp();
+            }
+        } while (wk.next());
+    }
+    // Tear-down.  Without a timeout every copy and product has been waited
+    // for; after one, what is in flight is (the drain has its own budget).
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort) {
+        int own = 0;
+        if (tid == 0) flag_status(a.hdr, DSPARK_DEV_TIMEOUT);
+        if (warp == 12) {
+            for (int u = max(0, issued - S); u < issued; ++u)
+                mbar_wait_bounded(&ms.raw_full[u % S], (u / S) & 1, &own, kWaitBudget);
+        } else if (warp == 13) {
+            if (elect_one()) mma_commit(&ms.drain);
+            __syncwarp();
+            mbar_wait_bounded(&ms.drain, 0, &own, kWaitBudget);
+        }
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+// Joins the parts of the item that CTA blockIdx.x left unfinished: a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) cache_attention_join(const AttnArgs a) {
+    const int32_t *d = a.desc + blockIdx.x * kDescInts;
+    const int rem = d[0];
+    if (rem <= 0) return;
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= d[3]) return;
+    const int parts = 1 + (rem + d[5] - 1) / d[5];
+    // Part 0 is this CTA's second slot, part i > 0 the first slot of CTA blockIdx.x + i.
+    auto slot = [&](int i) { return i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i); };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 v = a.part_ml[slot(i) * kRows + r];
+        m = fmaxf(m, v.x);
+    }
+    m = warp_max_f32(m);
+    constexpr int kPer = D / 32;
+    float o[kPer], l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const size_t at = (size_t)slot(i) * kRows + r;
+        const float2 v = a.part_ml[at];
+        const float w = v.x == -INFINITY ? (v.y == 0.f ? 0.f : v.y) : fast_exp2(v.x - m);   // y != 0 here is NaN
+        l = fmaf(w, v.y, l);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) o[k] = fmaf(w, a.part_o[at * D + k * 32 + lane], o[k]);
+    }
+    const int gr = d[2] + r;
+    const long long row = (long long)(d[1] + gr / a.group) * a.Hq + d[4] * a.group + gr % a.group;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        a.out[row * D + k * 32 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : o[k] / l * a.v_mul);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs &a, int grid, cudaStream_t st) {
+    const size_t bytes = Lay<D>::misc + (sizeof(Misc) + 15) / 16 * 16 + (size_t)(a.B + 1) * 4 + 1024;
+    cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)bytes);
+    if (e != cudaSuccess) return e;
+    cache_attention_kernel<D><<<grid, kThreads, bytes, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cache_attention_join<D><<<dim3(grid, kRows / 8), 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attention_ws_bytes(int D) {
+    return sizeof(WsHeader) + align256((size_t)kMaxCtas * kDescInts * 4) +
+           align256((size_t)2 * kMaxCtas * kRows * sizeof(float2)) + align256((size_t)2 * kMaxCtas * kRows * D * 4);
+}
+
+cudaError_t launch_cache_attention(AttnArgs a, void *ws, cudaStream_t st) {
+    uint8_t *p = static_cast<uint8_t *>(ws);
+    a.hdr = reinterpret_cast<WsHeader *>(p);
+    p += sizeof(WsHeader);
+    a.desc = reinterpret_cast<int32_t *>(p);
+    p += align256((size_t)kMaxCtas * kDescInts * 4);
+    a.part_ml = reinterpret_cast<float2 *>(p);
+    p += align256((size_t)2 * kMaxCtas * kRows * sizeof(float2));
+    a.part_o = reinterpret_cast<float *>(p);
+    a.budget = wait_budget(kWaitBudget);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+    return a.D == 128 ? launch_d<128>(a, grid, st) : launch_d<64>(a, grid, st);
+}
+
+}  // namespace dspark
