@@ -19,12 +19,13 @@
 //   O^T [D x rows]   += V^T P^T    A = V in shared memory, B = P
 //   L   [.. x rows]  += 1 P^T      A = ones in TMEM: the softmax sums, of the
 //                                  rounded P that the products use
-// Roles of the 14 warps (one CTA per SM, 512 TMEM columns):
+// Roles of the 16 warps (one CTA per SM, 512 TMEM columns):
 //   warps 0-3    keys: a thread turns one token's codes into f16 in its TMEM lane
 //   warps 4-7    values: one token's codes into f16 in shared memory (D-major operand)
-//   warps 8-11   softmax: a thread owns one key of the tile, all rows; queries; results
+//   warps 8-11   softmax: a thread owns one key of the tile, all rows; results
 //   warp 12      producer: page table, one bulk copy per page record
 //   warp 13      MMA issuer
+//   warps 14-15  queries of the next item, while this one runs
 // P is exp2 of the scaled score minus a running maximum that is only raised
 // (and O, L rescaled) when a score passes it by more than 8, so P <= 256 and
 // f16 keeps its 11 bits; K, V and Q (scaled by a power of two per row) are
@@ -42,7 +43,7 @@ using namespace tc;
 
 constexpr int kTile = 128;        // keys per tile
 constexpr int kRows = 64;         // query rows per item
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
 constexpr int kMaxCtas = 160;
 constexpr long long kWaitBudget = 4000000000LL;
 constexpr float kRaise = 8.f;     // log2 room above the running maximum
@@ -57,22 +58,30 @@ struct Lay {
     static constexpr int kVBytes = kTile * D * 2;
     static constexpr int kPBytes = kTile * kRows * 2;
     static constexpr int kQBytes = kRows * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int v = 0;
     static constexpr int p = v + 2 * kVBytes;
     static constexpr int q = p + 2 * kPBytes;
-    static constexpr int raw = q + kQBytes;
+    static constexpr int raw = q + 2 * kQBytes;
     static constexpr int misc = raw + kStages * kRec;
 };
 
-struct Misc {
-    float2 row[kRows];       // (multiplier of the raw score, running maximum)
+// What the softmax knows of an item's rows, two rows to an entry of `mul_m`:
+// the multipliers of their raw scores and their negated running maxima.
+struct Rows {
+    float4 mul_m[kRows / 2];
     int2 lim[kRows];         // visible keys [x, y)
     int orow[kRows];         // output row (token * Hq + head)
+    int nr, base, t0, t1, nt, q0, r0, h;   // the piece: rows, first key, its tiles of the item's nt, where it belongs
+    __device__ __forceinline__ float &mul(int r) { return reinterpret_cast<float *>(&mul_m[r / 2])[r & 1]; }
+    __device__ __forceinline__ float &neg_max(int r) { return reinterpret_cast<float *>(&mul_m[r / 2])[2 + (r & 1)]; }
+};
+struct Misc {
+    Rows rows[2];
     float fac[kRows];
     float wmax[4][kRows];
     uint64_t raw_full[8], raw_empty[8];
-    uint64_t k_full[2], s_full[2], v_full[2], p_full[2], pv_done[2], q_full, drain;
+    uint64_t k_full[2], s_full[2], v_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain;
     uint32_t tmem;
     int abort;
     int scan[16];
@@ -157,45 +166,69 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+// 16 columns of this thread's lane; the values are there after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 __device__ __forceinline__ float warp_max_f32(float v) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-// Bounded wait of a whole warp (converged again afterwards).  A try may sleep
-// for some microseconds, so a budget shorter than that is polled.
-__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
-    if (budget >= 1000000) {
-        mbar_wait_bounded(bar, parity, abort, budget);
-    } else {
-        const long long t0 = clock64();
-        for (;;) {
-            uint32_t ok;
+// Bounded wait of a whole warp (converged again afterwards).  The warps of a
+// CTA wait most of the time, and a polling warp takes issue slots from the
+// ones that work: a wait that does not succeed at once sleeps up to the hint
+// (ns) at a time.  Budgets shorter than such a sleep are polled.  The slow
+// part is a function: the roles' code together has to fit the instruction
+// cache.
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, long long budget) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok, stop;
+        if (budget >= 1000000)
             asm volatile(
-                "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
                 "selp.u32 %0, 1, 0, p;\n\t}"
                 : "=r"(ok)
-                : "r"(smem_u32(bar)), "r"(parity)
+                : "r"(bar), "r"(parity), "r"(10000000u)
                 : "memory");
-            if (ok || *abort) break;
-            if (clock64() - t0 > budget) {
-                *abort = 1;
-                break;
-            }
+        else
+            ok = bar_done(bar, parity);
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
+        if (ok || stop) break;
+        if (clock64() - t0 > budget) {
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
+            break;
         }
     }
+}
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
+    if (!bar_done(smem_u32(bar), parity))
+        wait_slow(smem_u32(bar), parity, smem_u32(const_cast<int *>(abort)), budget);
     __syncwarp();
 }
 // The 128 softmax threads.
@@ -214,12 +247,41 @@ __device__ __forceinline__ bool soft_any(bool v) {
         : "memory");
     return r != 0;
 }
-// 128-byte swizzled operand whose rows (128 bytes) run along K (the row
-// dimension is contiguous): 8-row groups 1024 bytes apart, 64-element blocks
-// of the row dimension `lbo` bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
-           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory operands in 128-byte swizzled rows, eight rows 1024 bytes
+// apart.  The descriptor's upper word is the same for all of them; the lower
+// word is the address and, for operands whose 64-element blocks of the row
+// dimension lie `lbo` bytes apart (D-major values, row-major probabilities),
+// that distance.  Adding bytes / 16 to the lower word moves the address.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return (saddr >> 4 & 0x3FFF) | (lbo >> 4) << 16;
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+// The products of one tile with the values and the ones.
+template <bool FIRST>
+__device__ __forceinline__ void mma_values(uint32_t tm, uint32_t v_lo, uint32_t p_lo, uint32_t id_o, uint32_t id_l) {
+    mma_ss<!FIRST>(tm + kColO, v_lo, p_lo, id_o);
+    mma_ts<!FIRST>(tm + kColL, tm + kColOne, p_lo, id_l);
+#pragma unroll
+    for (int kk = 1; kk < kTile / 16; ++kk) {
+        mma_ss<true>(tm + kColO, v_lo + kk * 128, p_lo + kk * 128, id_o);
+        mma_ts<true>(tm + kColL, tm + kColOne, p_lo + kk * 128, id_l);
+    }
 }
 // kind::f16 with f16 operands and fp32 sums, M = 128.
 __device__ __forceinline__ uint32_t idesc_f16(int N, bool a_mn, bool b_mn) {
@@ -238,11 +300,44 @@ __device__ __forceinline__ void unpack32(const uint4 c, uint32_t s0, uint32_t s1
     for (int i = 8; i < 16; ++i) r[i] = mul_f16x2(r[i], s1);
 }
 
+// The tile's probabilities of 16 * C rows from r0 for this thread's key: scores from
+// TMEM, 2^(score - maximum) in f16 to the P operand's row of the key.  Returns
+// the largest exponent.
+template <int C, bool MASKED>
+__device__ __forceinline__ float probs(uint32_t ts, const Rows &rw, uint8_t *prow, int r0, int key, int me) {
+    uint32_t s[C][16];
+#pragma unroll
+    for (int c = 0; c < C; ++c) tmem_ld16(ts + r0 + 16 * c, s[c]);
+    tmem_ld_wait();
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        uint32_t ph[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float4 mm = rw.mul_m[r0 / 2 + 8 * c + i / 2];
+            float2 x = fma2(make_float2(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])),
+                            make_float2(mm.x, mm.y), make_float2(mm.z, mm.w));
+            if (MASKED) {
+                const int4 l = *reinterpret_cast<const int4 *>(&rw.lim[r0 + 16 * c + i]);
+                if (me < l.x || me >= l.y) x.x = -INFINITY;
+                if (me < l.z || me >= l.w) x.y = -INFINITY;
+            }
+            top = max3(top, x.x, x.y);
+            const __half2 h2 = __floats2half2_rn(fast_exp2(x.x), fast_exp2(x.y));
+            ph[i / 2] = *reinterpret_cast<const uint32_t *>(&h2);
+        }
+        *reinterpret_cast<uint4 *>(prow + (((r0 / 8 + 2 * c) ^ (key & 7)) * 16)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+        *reinterpret_cast<uint4 *>(prow + (((r0 / 8 + 2 * c + 1) ^ (key & 7)) * 16)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+    }
+    return top;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const AttnArgs a) {
     using Y = Lay<D>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);   // still known to be shared memory
     Misc &ms = *reinterpret_cast<Misc *>(sm + Y::misc);
     int *prefix = reinterpret_cast<int *>(sm + Y::misc + (sizeof(Misc) + 15) / 16 * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -281,8 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
             mbar_init(&ms.v_full[i], 4);
             mbar_init(&ms.p_full[i], 4);
             mbar_init(&ms.pv_done[i], 1);
+            mbar_init(&ms.q_full[i], 2);
+            mbar_init(&ms.q_empty[i], 4);
         }
-        mbar_init(&ms.q_full, 4);
         mbar_init(&ms.drain, 1);
         fence_barrier_init();
     }
@@ -308,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     tc_fence_after();
     const uint32_t tm = ms.tmem;
     volatile int *abort = &ms.abort;
-    Walk wk(a, prefix, w0, w1);
+    const int tiles = w1 - w0;
     int g = 0;   // tiles done by this role
     int issued = 0;
 
@@ -324,29 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
             for (int i = 0; i < 16; ++i) one[i] = 0x3c003c00u;
             tmem_st16(tm + lane_base + kColOne, one);
         }
-        do {
-            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+        for (; g < tiles; ++g) {
                 const int st = g % S, bb = g & 1;
                 wait(&ms.raw_full[st], (g / S) & 1, abort, a.budget);
                 wait(&ms.s_full[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
                 tc_fence_after();
                 const uint8_t *raw = sm + Y::raw + st * Y::kRec;
-                uint32_t sc[D / 64];
-                if (D == 128) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(raw + soff);
-                    sc[0] = v.x;
-                    sc[D / 64 - 1] = v.y;
-                } else {
-                    sc[0] = *reinterpret_cast<const uint32_t *>(raw + soff);
-                }
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    const uint4 codes = *reinterpret_cast<const uint4 *>(raw + koff + c * a.P * 16);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; c += 2) {   // 64 dims: two pieces of codes, one word of scales
+                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(raw + soff + c * 2);
+                    const uint4 c0 = *reinterpret_cast<const uint4 *>(raw + koff + c * a.P * 16);
+                    const uint4 c1 = *reinterpret_cast<const uint4 *>(raw + koff + (c + 1) * a.P * 16);
                     uint32_t r[16];
-                    const uint32_t s0 = c & 1 ? scale_f16x2<2>(sc[c / 2]) : scale_f16x2<0>(sc[c / 2]);
-                    const uint32_t s1 = c & 1 ? scale_f16x2<3>(sc[c / 2]) : scale_f16x2<1>(sc[c / 2]);
-                    unpack32(codes, s0, s1, r);
+                    unpack32(c0, scale_f16x2<0>(sc), scale_f16x2<1>(sc), r);
                     tmem_st16(tm + lane_base + kColK + bb * 64 + c * 16, r);
+                    unpack32(c1, scale_f16x2<2>(sc), scale_f16x2<3>(sc), r);
+                    tmem_st16(tm + lane_base + kColK + bb * 64 + c * 16 + 16, r);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -355,42 +444,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     mbar_arrive(&ms.k_full[bb]);
                     mbar_arrive(&ms.raw_empty[st]);
                 }
-            }
-        } while (wk.next());
+        }
     } else if (warp < 8) {
         // -------------------------------------------------------- values
         const int key = tid - 128, R = record_bytes(a.P, D);
         const int half = half_bytes(a.P, D);
         const int voff = key / a.P * R + half + key % a.P * 16;
         const int soff = key / a.P * R + half + half_scales_off(a.P, D) + key % a.P * (D / 16);
-        do {
-            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+        for (; g < tiles; ++g) {
                 const int st = g % S, bb = g & 1;
                 wait(&ms.raw_full[st], (g / S) & 1, abort, a.budget);
                 wait(&ms.pv_done[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
                 const uint8_t *raw = sm + Y::raw + st * Y::kRec;
                 uint8_t *vrow = sm + Y::v + bb * Y::kVBytes + key * 128;
-                uint32_t sc[D / 64];
-                if (D == 128) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(raw + soff);
-                    sc[0] = v.x;
-                    sc[D / 64 - 1] = v.y;
-                } else {
-                    sc[0] = *reinterpret_cast<const uint32_t *>(raw + soff);
-                }
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    const uint4 codes = *reinterpret_cast<const uint4 *>(raw + voff + c * a.P * 16);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; c += 2) {
+                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(raw + soff + c * 2);
+                    const uint4 c0 = *reinterpret_cast<const uint4 *>(raw + voff + c * a.P * 16);
+                    const uint4 c1 = *reinterpret_cast<const uint4 *>(raw + voff + (c + 1) * a.P * 16);
                     uint32_t r[16];
-                    const uint32_t s0 = c & 1 ? scale_f16x2<2>(sc[c / 2]) : scale_f16x2<0>(sc[c / 2]);
-                    const uint32_t s1 = c & 1 ? scale_f16x2<3>(sc[c / 2]) : scale_f16x2<1>(sc[c / 2]);
-                    unpack32(codes, s0, s1, r);
+                    unpack32(c0, scale_f16x2<0>(sc), scale_f16x2<1>(sc), r);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int piece = ((c & 1) * 4 + u) ^ (key & 7);
-                        *reinterpret_cast<uint4 *>(vrow + (c / 2) * (kTile * 128) + piece * 16) =
+                    for (int u = 0; u < 4; ++u)
+                        *reinterpret_cast<uint4 *>(vrow + (u ^ (key & 7)) * 16) =
                             make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
-                    }
+                    unpack32(c1, scale_f16x2<2>(sc), scale_f16x2<3>(sc), r);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        *reinterpret_cast<uint4 *>(vrow + ((4 + u) ^ (key & 7)) * 16) =
+                            make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                    vrow += kTile * 128;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -398,63 +481,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     mbar_arrive(&ms.v_full[bb]);
                     mbar_arrive(&ms.raw_empty[st]);
                 }
-            }
-        } while (wk.next());
+        }
     } else if (warp < 12) {
         // ------------------------------------------------------- softmax
         const int key = tid - 256, sw = warp - 8;
         const uint32_t lane_base = (uint32_t)(sw * 32) << 16;
         if (key == 0) a.desc[blockIdx.x * kDescInts] = 0;
+        int piece = 0;
         do {
-            const int nr = wk.k.nr, N = (nr + 15) / 16 * 16;
-            // Queries: D / 8 lanes a row, scaled by a power of two so that f16 holds them exactly.
-            {
-                constexpr int kLanes = D / 8, kPass = 128 / kLanes;
-                const int piece = key % kLanes;
-                for (int r = key / kLanes; r < N; r += kPass) {
-                    const bool live = r < nr;
-                    const int gr = wk.k.r0 + r, j = gr / a.group, hd = wk.h * a.group + gr % a.group;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (live)
-                        w = *reinterpret_cast<const uint4 *>(a.q + (long long)(wk.q.q0 + j) * a.q_stride + hd * D +
-                                                             piece * 8);
-                    float f[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y),
-                                  bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
-                    float mx = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[i]));
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // 2^e * max in [2^14, 2^15); e within fp32's exponents.
-                    const int ex = (int)(__float_as_uint(mx) >> 23) - 127;
-                    const int e = (mx > 0.f && ex < 128) ? min(14 - ex, 100) : 0;
-                    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    uint32_t hh[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __half2 x = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
-                        hh[i] = *reinterpret_cast<const uint32_t *>(&x);
-                    }
-                    *reinterpret_cast<uint4 *>(sm + Y::q + (piece / 8) * (kRows * 128) + r * 128 +
-                                               (((piece & 7) ^ (r & 7)) * 16)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-                    if (piece == 0) {
-                        const int pos = wk.q.L - wk.q.n + j;
-                        ms.row[r] = live ? make_float2(a.qk_mul * down, -INFINITY) : make_float2(0.f, 0.f);
-                        ms.lim[r] = live ? make_int2(a.window > 0 ? max(0, pos - a.window + 1) : 0, pos + 1)
-                                         : make_int2(0, 0);
-                        ms.orow[r] = (wk.q.q0 + j) * a.Hq + hd;
-                    }
-                }
-                fence_proxy_async_smem();
-                soft_sync();
-                if (lane == 0) mbar_arrive(&ms.q_full);
-            }
+            Rows &rw = ms.rows[piece & 1];
+            wait(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
+            if (soft_any(*abort != 0)) break;   // the piece may not be there: the four warps leave together
+            const int nr = rw.nr, N = (nr + 15) / 16 * 16, t0 = rw.t0, t1 = rw.t1;
             // Tiles that every row sees whole need no mask.
-            const int all_hi = ms.lim[0].y, all_lo = ms.lim[nr - 1].x;
-            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
+            const int all_hi = rw.lim[0].y, all_lo = rw.lim[nr - 1].x;
+            for (int t = t0; t < t1; ++t, ++g) {
                 const int bb = g & 1;
-                const int kpos = wk.k.base + t * kTile;
+                const int kpos = rw.base + t * kTile;
                 const bool masked = kpos + kTile > all_hi || kpos < all_lo;
                 const int me = kpos + key;
                 uint8_t *prow = sm + Y::p + bb * Y::kPBytes + key * 128;
@@ -462,73 +505,72 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                 wait(&ms.s_full[bb], (g >> 1) & 1, abort, a.budget);
                 wait(&ms.pv_done[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
                 tc_fence_after();
-                bool raise = t == wk.t0;
-                for (int pass = 0;; ++pass) {
+                bool raise = t == t0;
+                for (;;) {
                     if (raise) {
                         // New maxima over the tile: a warp's 32 keys, then the four warps.
-                        for (int c = 0; c < N; c += 16) {
-                            float s[16];
-                            tmem_ld16(ts + c, s);
+#pragma unroll 1
+                        for (int r0 = 0; r0 < N; r0 += 4) {
+                            uint32_t s[4];
+                            tmem_ld4(ts + r0, s);
+                            tmem_ld_wait();
+                            float x[4];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float x = s[i] * ms.row[c + i].x;
+                            for (int i = 0; i < 4; ++i) {
+                                x[i] = __uint_as_float(s[i]) * rw.mul(r0 + i);
                                 if (masked) {
-                                    const int2 l = ms.lim[c + i];
-                                    if (me < l.x || me >= l.y) x = -INFINITY;
+                                    const int2 l = rw.lim[r0 + i];
+                                    if (me < l.x || me >= l.y) x[i] = -INFINITY;
                                 }
-                                x = warp_max_f32(x);
-                                if (lane == i) ms.wmax[sw][c + i] = x;
+                                x[i] = warp_max_f32(x[i]);
                             }
+                            if (lane == 0)
+                                *reinterpret_cast<float4 *>(&ms.wmax[sw][r0]) = make_float4(x[0], x[1], x[2], x[3]);
                         }
                         soft_sync();
                         if (key < N) {
-                            const float old = ms.row[key].y;
+                            float &neg = rw.neg_max(key);
+                            const float old = -neg;
                             const float nm = fmaxf(fmaxf(fmaxf(ms.wmax[0][key], ms.wmax[1][key]),
                                                          fmaxf(ms.wmax[2][key], ms.wmax[3][key])), old);
                             ms.fac[key] = nm == old ? 1.f : fast_exp2(old - nm);
-                            ms.row[key].y = nm;
+                            neg = -nm;
                         }
                         soft_sync();
-                        if (t > wk.t0) {
+                        if (t > t0) {
                             wait(&ms.pv_done[bb ^ 1], ((g - 1) >> 1) & 1, abort, a.budget);
                             tc_fence_after();
-                            for (int c = 0; c < N; c += 16) {
+#pragma unroll 1
+                            for (int r0 = 0; r0 < N; r0 += 4) {
+                                uint32_t o[4], l[4];
+                                tmem_ld4(tm + lane_base + kColO + r0, o);
+                                tmem_ld4(tm + lane_base + kColL + r0, l);
+                                tmem_ld_wait();
 #pragma unroll
-                                for (int w = 0; w < 2; ++w) {
-                                    const uint32_t at = tm + lane_base + (w ? kColL : kColO) + c;
-                                    float o[16];
-                                    uint32_t u[16];
-                                    tmem_ld16(at, o);
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * ms.fac[c + i]);
-                                    tmem_st16(at, u);
+                                for (int i = 0; i < 4; ++i) {
+                                    const float f = ms.fac[r0 + i];
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    l[i] = __float_as_uint(__uint_as_float(l[i]) * f);
                                 }
+                                tmem_st4(tm + lane_base + kColO + r0, o);
+                                tmem_st4(tm + lane_base + kColL + r0, l);
                             }
                             tmem_st_wait();
                         }
                     }
-                    float top = -INFINITY;
-                    for (int c = 0; c < N; c += 16) {
-                        float s[16];
-                        tmem_ld16(ts + c, s);
-                        uint32_t ph[8];
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 rm = *reinterpret_cast<const float4 *>(&ms.row[c + i]);
-                            float x0 = fmaf(s[i], rm.x, -rm.y), x1 = fmaf(s[i + 1], rm.z, -rm.w);
-                            if (masked) {
-                                const int4 l = *reinterpret_cast<const int4 *>(&ms.lim[c + i]);
-                                if (me < l.x || me >= l.y) x0 = -INFINITY;
-                                if (me < l.z || me >= l.w) x1 = -INFINITY;
-                            }
-                            top = max3(top, x0, x1);
-                            const __half2 h2 = __floats2half2_rn(fast_exp2(x0), fast_exp2(x1));
-                            ph[i / 2] = *reinterpret_cast<const uint32_t *>(&h2);
-                        }
-                        *reinterpret_cast<uint4 *>(prow + (((c / 8) ^ (key & 7)) * 16)) =
-                            make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                        *reinterpret_cast<uint4 *>(prow + (((c / 8 + 1) ^ (key & 7)) * 16)) =
-                            make_uint4(ph[4], ph[5], ph[6], ph[7]);
+                    float top;
+                    if (masked) {   // rare: one code for every number of rows
+                        top = -INFINITY;
+                        for (int c = 0; c < N; c += 16)
+                            top = fmaxf(top, probs<1, true>(ts, rw, prow, c, key, me));
+                    } else if (N == 16) {
+                        top = probs<1, false>(ts, rw, prow, 0, key, me);
+                    } else if (N == 32) {
+                        top = probs<2, false>(ts, rw, prow, 0, key, me);
+                    } else if (N == 48) {
+                        top = probs<3, false>(ts, rw, prow, 0, key, me);
+                    } else {
+                        top = probs<4, false>(ts, rw, prow, 0, key, me);
                     }
                     if (raise) break;                       // at most one raise a tile
                     raise = soft_any(top > kRaise);
@@ -542,42 +584,48 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
             // The piece's result: this thread's dim of every row.
             wait(&ms.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, a.budget);
             tc_fence_after();
-            const bool whole = wk.t0 == 0 && wk.t1 == wk.k.nt;
-            const int slot = 2 * blockIdx.x + (wk.t0 == 0 ? 1 : 0);
-            for (int c = 0; c < N; c += 16) {
-                float o[16], l[16];
-                tmem_ld16(tm + lane_base + kColO + c, o);
-                tmem_ld16(tm + lane_base + kColL + c, l);
+            const bool whole = t0 == 0 && t1 == rw.nt;
+            const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+#pragma unroll 1
+            for (int r0 = 0; r0 < nr; r0 += 4) {   // a short loop: code that runs once an item is fetched anew each time
+                uint32_t o[4], l[4];
+                tmem_ld4(tm + lane_base + kColO + r0, o);
+                tmem_ld4(tm + lane_base + kColL + r0, l);
+                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = c + i;
-                    if (r < nr) {
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + i;
+                    const float oo = __uint_as_float(o[i]), ll = __uint_as_float(l[i]);
+                    if (r < nr && key < D) {
                         if (whole) {
-                            const float y = l[i] == 0.f ? 0.f : o[i] / l[i] * a.v_mul;
-                            if (key < D) a.out[(long long)ms.orow[r] * D + key] = __float2bfloat16_rn(y);
+                            const float y = ll == 0.f ? 0.f : oo * __fdividef(a.v_mul, ll);
+                            a.out[(long long)rw.orow[r] * D + key] = __float2bfloat16_rn(y);
                         } else {
-                            if (key < D) a.part_o[((size_t)slot * kRows + r) * D + key] = o[i];
-                            if (key == 0) a.part_ml[slot * kRows + r] = make_float2(ms.row[r].y, l[i]);
+                            a.part_o[((size_t)slot * kRows + r) * D + key] = oo;
+                            if (key == 0) a.part_ml[slot * kRows + r] = make_float2(-rw.neg_max(r), ll);
                         }
                     }
                 }
             }
-            if (!whole && wk.t0 == 0 && key == 0) {
+            if (!whole && t0 == 0 && key == 0) {
                 int32_t *d = a.desc + blockIdx.x * kDescInts;
-                d[1] = wk.q.q0;
-                d[2] = wk.k.r0;
+                d[1] = rw.q0;
+                d[2] = rw.r0;
                 d[3] = nr;
-                d[4] = wk.h;
+                d[4] = rw.h;
                 d[5] = quota;
-                d[0] = wk.k.nt - wk.t1;
+                d[0] = rw.nt - t1;
             }
             tc_fence_before();
-            soft_sync();   // before the rows' state is rewritten
-        } while (wk.next());
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_empty[piece & 1]);
+            ++piece;
+        } while (g < tiles);
     } else if (warp == 12) {
         // ------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
         const int R = record_bytes(a.P, D), ppt = kTile / a.P;
+        Walk wk(a, prefix, w0, w1);
         do {
             for (int t = wk.t0; t < wk.t1; ++t, ++g) {
                 const int st = g % S;
@@ -603,53 +651,134 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                 }
             }
         } while (wk.next());
-    } else {
+    } else if (warp == 13) {
         // ----------------------------------------------------------- MMA
         int piece = 0;
-        const uint32_t qb = smem_u32(sm + Y::q);
+        // D = 64: the second 64 rows of the value operand repeat the first (their lanes are not read).
+        const uint32_t v0 = desc_lo(smem_u32(sm + Y::v), D == 128 ? kTile * 128 : 0);
+        const uint32_t p0 = desc_lo(smem_u32(sm + Y::p), 0), q0 = desc_lo(smem_u32(sm + Y::q), 16);
         do {
-            const int N = (wk.k.nr + 15) / 16 * 16;
+            wait(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
+            if (__shfl_sync(0xffffffffu, *abort, 0)) break;
+            const Rows &rw = ms.rows[piece & 1];
+            const int N = (rw.nr + 15) / 16 * 16, g_end = g + rw.t1 - rw.t0;
             const uint32_t id_s = idesc_f16(N, false, false), id_o = idesc_f16(N, true, true),
                            id_l = idesc_f16(N, false, true);
-            wait(&ms.q_full, piece & 1, abort, a.budget);
+            const uint32_t q_lo = q0 + (piece & 1) * (Y::kQBytes / 16);
             ++piece;
-            const int g_end = g + (wk.t1 - wk.t0);
-            auto scores = [&](int gg) {
-                const int bb = gg & 1;
-                wait(&ms.k_full[bb], (gg >> 1) & 1, abort, a.budget);
-                tc_fence_after();
-                const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
-                if (go && elect_one()) {
+            bool first = true;
+            // One step ahead with the scores: step x issues the scores of tile x and the values of tile x - 1.
+            for (int x = g; x <= g_end; ++x) {
+                if (x < g_end) {
+                    const int bb = x & 1;
+                    wait(&ms.k_full[bb], (x >> 1) & 1, abort, a.budget);
+                    tc_fence_after();
+                    const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
+                    if (go && elect_one()) {
+                        const uint32_t ds = tm + kColS + bb * 64, dk = tm + kColK + bb * 64;
+                        mma_ts<false>(ds, dk, q_lo, id_s);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        mma_bf16_ts(tm + kColS + bb * 64, tm + kColK + bb * 64 + kk * 8,
-                                    sw128_desc(qb + (kk / 4) * (kRows * 128) + (kk & 3) * 32), id_s, kk > 0);
-                    mma_commit(&ms.s_full[bb]);
-                }
-                __syncwarp();
-            };
-            scores(g);
-            for (bool first = true; g < g_end; ++g, first = false) {
-                if (g + 1 < g_end) scores(g + 1);
-                const int bb = g & 1;
-                wait(&ms.v_full[bb], (g >> 1) & 1, abort, a.budget);
-                wait(&ms.p_full[bb], (g >> 1) & 1, abort, a.budget);
-                tc_fence_after();
-                const uint32_t vb = smem_u32(sm + Y::v + bb * Y::kVBytes), pb = smem_u32(sm + Y::p + bb * Y::kPBytes);
-                const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
-                if (go && elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk) {
-                        const uint64_t pd = sw128_desc_mn(pb + kk * 2048, 0);
-                        const uint32_t acc = !first || kk > 0;
-                        // D = 64: the second 64 rows of the operand repeat the first (their lanes are not read).
-                        mma_bf16(tm + kColO, sw128_desc_mn(vb + kk * 2048, D == 128 ? kTile * 128 : 0), pd, id_o, acc);
-                        mma_bf16_ts(tm + kColL, tm + kColOne, pd, id_l, acc);
+                        for (int kk = 1; kk < D / 16; ++kk)
+                            mma_ts<true>(ds, dk + kk * 8, q_lo + (kk / 4) * (kRows * 8) + (kk & 3) * 2, id_s);
+                        mma_commit(&ms.s_full[bb]);
                     }
-                    mma_commit(&ms.pv_done[bb]);
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (x > g) {
+                    const int bb = (x - 1) & 1, ph = ((x - 1) >> 1) & 1;
+                    wait(&ms.v_full[bb], ph, abort, a.budget);
+                    wait(&ms.p_full[bb], ph, abort, a.budget);
+                    tc_fence_after();
+                    const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
+                    if (go && elect_one()) {
+                        const uint32_t v_lo = v0 + bb * (Y::kVBytes / 16), p_lo = p0 + bb * (Y::kPBytes / 16);
+                        if (first)
+                            mma_values<true>(tm, v_lo, p_lo, id_o, id_l);
+                        else
+                            mma_values<false>(tm, v_lo, p_lo, id_o, id_l);
+                        mma_commit(&ms.pv_done[bb]);
+                    }
+                    __syncwarp();
+                    first = false;
+                }
             }
+            g = g_end;
+        } while (g < tiles);
+    } else {
+        // ------------------------------------------------------- queries
+        // D / 8 lanes a row; scaled by a power of two so that f16 holds them exactly.
+        constexpr int kLanes = D / 8, kPass = 64 / kLanes, kBatch = 4;
+        const int id = tid - 14 * 32, part = id % kLanes;
+        int piece = 0;
+        Walk wk(a, prefix, w0, w1);
+        do {
+            Rows &rw = ms.rows[piece & 1];
+            uint8_t *qs = sm + Y::q + (piece & 1) * Y::kQBytes;
+            const int nr = wk.k.nr, N = (nr + 15) / 16 * 16;
+            wait(&ms.q_empty[piece & 1], ((piece >> 1) & 1) ^ 1, abort, a.budget);
+            if (id == 0) {
+                rw.nr = nr;
+                rw.base = wk.k.base;
+                rw.t0 = wk.t0;
+                rw.t1 = wk.t1;
+                rw.nt = wk.k.nt;
+                rw.q0 = wk.q.q0;
+                rw.r0 = wk.k.r0;
+                rw.h = wk.h;
+            }
+#pragma unroll 1
+            for (int rr = id / kLanes; rr < N; rr += kPass * kBatch) {
+                uint4 w[kBatch];
+                int j[kBatch], hd[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = rr + u * kPass, gr = wk.k.r0 + r;
+                    j[u] = gr / a.group;
+                    hd[u] = wk.h * a.group + gr - j[u] * a.group;
+                    w[u] = make_uint4(0, 0, 0, 0);
+                    if (r < nr)
+                        w[u] = __ldg(reinterpret_cast<const uint4 *>(a.q + (long long)(wk.q.q0 + j[u]) * a.q_stride +
+                                                                     hd[u] * D + part * 8));
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = rr + u * kPass;
+                    if (r >= N) continue;   // N is a multiple of 16: whole warps
+                    const float f[8] = {bf16lo(w[u].x), bf16hi(w[u].x), bf16lo(w[u].y), bf16hi(w[u].y),
+                                        bf16lo(w[u].z), bf16hi(w[u].z), bf16lo(w[u].w), bf16hi(w[u].w)};
+                    float mx = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[i]));
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // 2^e * max in [2^14, 2^15); e within fp32's exponents.
+                    const int ex = (int)(__float_as_uint(mx) >> 23) - 127;
+                    const int e = (mx > 0.f && ex < 128) ? min(14 - ex, 100) : 0;
+                    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    uint32_t hh[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2 x = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+                        hh[i] = *reinterpret_cast<const uint32_t *>(&x);
+                    }
+                    *reinterpret_cast<uint4 *>(qs + (part / 8) * (kRows * 128) + r * 128 +
+                                               (((part & 7) ^ (r & 7)) * 16)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                    if (part == 0) {
+                        const bool live = r < nr;
+                        const int pos = wk.q.L - wk.q.n + j[u];
+                        rw.mul(r) = live ? a.qk_mul * down : 0.f;
+                        rw.neg_max(r) = live ? INFINITY : 0.f;
+                        rw.lim[r] = live ? make_int2(a.window > 0 ? max(0, pos - a.window + 1) : 0, pos + 1)
+                                         : make_int2(0, 0);
+                        rw.orow[r] = (wk.q.q0 + j[u]) * a.Hq + hd[u];
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_full[piece & 1]);
+            ++piece;
         } while (wk.next());
     }
     // Tear-down.  Without a timeout every copy and product has been waited
