@@ -1,5 +1,5 @@
 // cache_attention.cu -- attention of the target pass over the paged 4-bit
-// cache (tcgen05 / TMEM / bulk copies).
+// cache (tcgen05 / TMEM / cp.async).
 //
 // For query row r (token j of request b, head hq; its key head h = hq / group)
 // at position p_r = kv_len[b] - n_b + j, over the keys i it may see
@@ -19,13 +19,23 @@
 //   O^T [D x rows]   += V^T P^T    A = V in shared memory, B = P
 //   L   [.. x rows]  += 1 P^T      A = ones in TMEM: the softmax sums, of the
 //                                  rounded P that the products use
-// Roles of the 16 warps (one CTA per SM, 512 TMEM columns):
-//   warps 0-3    keys: a thread turns one token's codes into f16 in its TMEM lane
-//   warps 4-7    values: one token's codes into f16 in shared memory (D-major operand)
-//   warps 8-11   softmax: a thread owns one key of the tile, all rows; results
-//   warp 12      producer: page table, one bulk copy per page record
-//   warp 13      MMA issuer
-//   warps 14-15  queries of the next item, while this one runs
+// Three groups of four warps take the tiles in turn, and a group does all of
+// a tile's arithmetic, a thread per key: its K codes into f16 in TMEM, the
+// probabilities of all rows when the scores are there, its V codes into f16 in
+// shared memory; the group that ends an item writes its result.  So a tile
+// costs a warp six waits, and while one group waits for its products the
+// others work.  (With a role per step -- keys, values, softmax in 24 warps --
+// the waits and hand-overs were half of all instructions, and a tile took
+// 1700 cycles.)  Four more warps:
+//   12  pages: the tiles' record addresses from the block table, ahead of use
+//   13  issues the score MMAs
+//   14  issues the MMAs with the values and the ones
+//   15  queries of the next item, while this one runs
+// An issuing thread stands still while its MMAs queue, and a wait costs it
+// some hundred cycles, so the two products have a thread each.
+// A thread copies the codes of its own key with cp.async, one own tile ahead,
+// so no barrier stands between copy and use.  (A producer warp with two bulk
+// copies per page took 2200 cycles a tile: it was what bounded the kernel.)
 // P is exp2 of the scaled score minus a running maximum that is only raised
 // (and O, L rescaled) when a score passes it by more than 8, so P <= 256 and
 // f16 keeps its 11 bits; K, V and Q (scaled by a power of two per row) are
@@ -42,28 +52,32 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;        // keys per tile
-constexpr int kRows = 64;         // query rows per item
-constexpr int kThreads = 512;
+constexpr int kRows = 48;         // query rows per item (six tokens of groups of eight)
+constexpr int kGroups = 3;        // groups of four warps: tiles under way
+constexpr int kRing = 4;          // buffers of scores and of probabilities: one more, so that a group need not
+                                  // wait for its last tile's products
+constexpr int kAhead = 16;        // tiles whose pages are known
+constexpr int kWarpLoad = 4 * kGroups, kWarpQk = kWarpLoad + 1, kWarpPv = kWarpLoad + 2;   // the last warp: queries
+constexpr int kThreads = (kWarpLoad + 4) * 32;
 constexpr int kMaxCtas = 160;
 constexpr long long kWaitBudget = 4000000000LL;
 constexpr float kRaise = 8.f;     // log2 room above the running maximum
 constexpr int kDescInts = 8;      // rem, q0, r0, nr, h, quota
 
 // TMEM columns.
-constexpr int kColK = 0, kColS = 128, kColO = 256, kColL = 320, kColOne = 384;
+constexpr int kColK = 0, kColS = 192, kColO = 384, kColL = 432, kColOne = 480;
 
 template <int D>
 struct Lay {
-    static constexpr int kRec = kTile * D / 8 * 9;       // bytes of one tile's records
     static constexpr int kVBytes = kTile * D * 2;
-    static constexpr int kPBytes = kTile * kRows * 2;
+    static constexpr int kPBytes = kTile * 128;         // a 128-byte row per key
     static constexpr int kQBytes = kRows * D * 2;
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kHalf = kTile * D / 16 * 9;     // one tile's K (or V) codes [D/32][128][16], then scales
     static constexpr int v = 0;
     static constexpr int p = v + 2 * kVBytes;
-    static constexpr int q = p + 2 * kPBytes;
-    static constexpr int raw = q + 2 * kQBytes;
-    static constexpr int misc = raw + kStages * kRec;
+    static constexpr int q = p + kRing * kPBytes;
+    static constexpr int raw = q + 2 * kQBytes;           // per group: K half, V half
+    static constexpr int misc = raw + kGroups * 2 * kHalf;
 };
 
 // What the softmax knows of an item's rows, two rows to an entry of `mul_m`:
@@ -73,15 +87,21 @@ struct Rows {
     int2 lim[kRows];         // visible keys [x, y)
     int orow[kRows];         // output row (token * Hq + head)
     int nr, base, t0, t1, nt, q0, r0, h;   // the piece: rows, first key, its tiles of the item's nt, where it belongs
+    int version;             // times the maxima were raised
     __device__ __forceinline__ float &mul(int r) { return reinterpret_cast<float *>(&mul_m[r / 2])[r & 1]; }
     __device__ __forceinline__ float &neg_max(int r) { return reinterpret_cast<float *>(&mul_m[r / 2])[2 + (r & 1)]; }
 };
 struct Misc {
     Rows rows[2];
-    float fac[kRows];
-    float wmax[4][kRows];
-    uint64_t raw_full[8], raw_empty[8];
-    uint64_t k_full[2], s_full[2], v_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain;
+    float fac[kGroups][kRows];
+    float wmax[kGroups][4][kRows];
+    unsigned long long rec[kAhead][8];   // a tile's page records (0: no keys there)
+    uint64_t rec_full[kAhead], rec_empty[kAhead];
+    // Per group: its keys are in TMEM; its scores are there; it has had its turn at the maxima and O.
+    uint64_t k_full[kGroups], s_full[kGroups], turn[kGroups];
+    // Per tile of the ring: P and V are in shared memory; the products are done.
+    uint64_t vp_full[kRing], pv_done[kRing];
+    uint64_t q_full[2], q_empty[2], m_full[2], drain[2];   // m_full: the piece's first maxima are set
     uint32_t tmem;
     int abort;
     int scan[16];
@@ -100,14 +120,17 @@ __device__ __forceinline__ Req load_req(const AttnArgs &a, int b) {
     return r;
 }
 
-// Row block rb of a request: rows [r0, r0 + nr), keys [base, hi) in tiles.
+// Row block rb of a request: its rows in equal blocks of at most kRows; rows
+// [r0, r0 + nr), keys [base, hi) in tiles.
 struct Block {
     int r0, nr, base, hi, nt;
 };
+__device__ __forceinline__ int row_blocks(const AttnArgs &a, const Req &q) { return (q.n * a.group + kRows - 1) / kRows; }
 __device__ __forceinline__ Block row_block(const AttnArgs &a, const Req &q, int rb) {
     Block k;
-    k.r0 = rb * kRows;
-    k.nr = min(kRows, q.n * a.group - k.r0);
+    const int rows = q.n * a.group, nb = row_blocks(a, q);
+    k.r0 = (int)((long long)rows * rb / nb);
+    k.nr = (int)((long long)rows * (rb + 1) / nb) - k.r0;
     const int jf = k.r0 / a.group, jl = (k.r0 + k.nr - 1) / a.group;
     k.hi = max(0, q.L - q.n + jl + 1);
     const int lo = a.window > 0 ? max(0, q.L - q.n + jf - a.window + 1) : 0;
@@ -147,7 +170,7 @@ struct Walk {
         if (left <= 0) return false;
         if (++h == a.Hkv) {
             h = 0;
-            if ((rb + 1) * kRows < q.n * a.group) {
+            if (rb + 1 < row_blocks(a, q)) {
                 ++rb;
             } else {
                 rb = 0;
@@ -185,6 +208,11 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+__device__ __forceinline__ float rcp(float x) {   // within 1 ulp
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ float warp_max_f32(float v) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -205,45 +233,51 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, long long budget) {
+// Returns false when the wait ran out, here or in another role.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, long long budget) {
     const long long t0 = clock64();
     for (;;) {
         uint32_t ok, stop;
         if (budget >= 1000000)
             asm volatile(
-                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
+                "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 32;\nTRY%=:\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE%=;\n\tsub.u32 n, n, 1;\n\t"
+                "setp.ne.u32 q, n, 0;\n\t@q bra TRY%=;\nDONE%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
                 : "=r"(ok)
-                : "r"(bar), "r"(parity), "r"(10000000u)
+                : "r"(bar), "r"(parity)
                 : "memory");
         else
             ok = bar_done(bar, parity);
+        if (ok) return true;
         asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
-        if (ok || stop) break;
+        if (stop) return false;
         if (clock64() - t0 > budget) {
             asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
-            break;
+            return false;
         }
     }
 }
+__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
+    return bar_done(smem_u32(bar), parity) ||
+           wait_slow(smem_u32(bar), parity, smem_u32(const_cast<int *>(abort)), budget);
+}
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
-    if (!bar_done(smem_u32(bar), parity))
-        wait_slow(smem_u32(bar), parity, smem_u32(const_cast<int *>(abort)), budget);
+    wait1(bar, parity, abort, budget);
     __syncwarp();
 }
-// The 128 softmax threads.
-__device__ __forceinline__ void soft_sync() {
+// The 128 threads of softmax group sg.
+__device__ __forceinline__ void soft_sync(int sg) {
     __syncwarp();
-    asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(sg + 1) : "memory");
 }
-__device__ __forceinline__ bool soft_any(bool v) {
+__device__ __forceinline__ bool soft_any(int sg, bool v) {
     uint32_t r;
     __syncwarp();
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.aligned.pred p, 1, 128, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.or.aligned.pred p, %2, 128, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "r"(sg + 1)
         : "memory");
     return r != 0;
 }
@@ -288,6 +322,13 @@ __device__ __forceinline__ uint32_t idesc_f16(int N, bool a_mn, bool b_mn) {
     return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
+__device__ __forceinline__ void cp_async16(uint8_t *dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+template <int BYTES>   // 4 or 8
+__device__ __forceinline__ void cp_async_scales(uint8_t *dst, const uint8_t *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
 // 16 bytes of codes and two scales -> 16 f16x2.
 __device__ __forceinline__ void unpack32(const uint4 c, uint32_t s0, uint32_t s1, uint32_t (&r)[16]) {
     e2m1x8_to_f16(c.x, r[0], r[1], r[2], r[3]);
@@ -339,9 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);   // still known to be shared memory
     Misc &ms = *reinterpret_cast<Misc *>(sm + Y::misc);
-    int *prefix = reinterpret_cast<int *>(sm + Y::misc + (sizeof(Misc) + 15) / 16 * 16);
+    // In the probabilities' place: the walks that read it are set up before the
+    // first scores, and so before the first probabilities.
+    int *prefix = reinterpret_cast<int *>(sm + Y::p);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int S = Y::kStages;
 
     // Tiles of every request, and their prefix: thread t sums a run of requests.
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -352,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         const Req q = load_req(a, b);
         bad |= __ldg(a.kv_len + b) != q.L || __ldg(a.q_start + b) != q.q0 || __ldg(a.q_start + b + 1) != q.q0 + q.n;
         int t = 0;
-        for (int rb = 0; rb * kRows < q.n * a.group; ++rb) t += row_block(a, q, rb).nt;
+        for (int rb = 0; rb < row_blocks(a, q); ++rb) t += row_block(a, q, rb).nt;
         prefix[b] = sum;
         sum += t * a.Hkv;
     }
@@ -366,20 +408,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     if (lane == 31) ms.scan[warp] = inc;
     if (tid == 0) {
         ms.abort = 0;
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&ms.raw_full[i], 1);
-            mbar_init(&ms.raw_empty[i], 8);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(&ms.rec_full[i], 1);
+            mbar_init(&ms.rec_empty[i], 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
             mbar_init(&ms.k_full[i], 4);
             mbar_init(&ms.s_full[i], 1);
-            mbar_init(&ms.v_full[i], 4);
-            mbar_init(&ms.p_full[i], 4);
-            mbar_init(&ms.pv_done[i], 1);
-            mbar_init(&ms.q_full[i], 2);
-            mbar_init(&ms.q_empty[i], 4);
+            mbar_init(&ms.turn[i], 4);
         }
-        mbar_init(&ms.drain, 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&ms.vp_full[i], 4);
+            mbar_init(&ms.pv_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.q_full[i], 1);
+            mbar_init(&ms.q_empty[i], 4 * kGroups);
+            mbar_init(&ms.m_full[i], 4);
+            mbar_init(&ms.drain[i], 1);
+        }
         fence_barrier_init();
     }
     __syncthreads();
@@ -395,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         if (tid == 0) a.desc[blockIdx.x * kDescInts] = 0;
         return;
     }
+    if (tid == 0) a.desc[blockIdx.x * kDescInts] = 0;   // an unfinished last item replaces it below
     if (warp == 0) {
         tmem_alloc(&ms.tmem, 512);
         tmem_relinquish();
@@ -406,111 +454,133 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     volatile int *abort = &ms.abort;
     const int tiles = w1 - w0;
     int g = 0;   // tiles done by this role
-    int issued = 0;
 
-    if (warp < 4) {
-        // ---------------------------------------------------------- keys
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const int key = tid, R = record_bytes(a.P, D);
-        const int koff = key / a.P * R + key % a.P * 16;
-        const int soff = key / a.P * R + half_scales_off(a.P, D) + key % a.P * (D / 16);
-        {
+    if (warp < 4 * kGroups) {
+        // ----------------------------------------------- keys, softmax, values
+        // Group sg takes the tiles g with g % kGroups == sg.  The groups share
+        // the rows' maxima and O: tile g's probabilities are given to the
+        // products only after tile g - 1 had its turn, and computed anew in the
+        // rare case that its turn raised a maximum.
+        const int key = tid & 127, sw = warp & 3, sg = warp >> 2;
+        const uint32_t lane_base = (uint32_t)(sw * 32) << 16;
+        // A thread copies the codes and scales of its own key, one own tile
+        // ahead, so it waits for its own copies only.
+        uint8_t *kraw = sm + Y::raw + sg * 2 * Y::kHalf + key * 16, *vraw = kraw + Y::kHalf;
+        constexpr int kScaleAt = kTile * D / 2;
+        uint8_t *kscale = kraw + kScaleAt - key * 16 + key * (D / 16), *vscale = kscale + Y::kHalf;
+        const int off = key % a.P, hb = half_bytes(a.P, D), soff = half_scales_off(a.P, D) + off * (D / 16);
+        auto find = [&](int x) -> unsigned long long {      // this key's record in tile x
+            unsigned long long r = 0;
+            if (x < tiles) {
+                // Only what the producer has published is an address.
+                if (wait1(&ms.rec_full[x % kAhead], (x / kAhead) & 1, abort, a.budget)) r = ms.rec[x % kAhead][key / a.P];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.rec_empty[x % kAhead]);
+            }
+            return r;
+        };
+        auto copy = [&](unsigned long long from, uint8_t *codes, uint8_t *scales) {
+            if (from != 0) {
+                const uint8_t *p = reinterpret_cast<const uint8_t *>(from) + off * 16;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) cp_async16(codes + c * (kTile * 16), p + c * a.P * 16);
+                cp_async_scales<D / 16>(scales, reinterpret_cast<const uint8_t *>(from) + soff);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            __syncwarp();   // lanes whose pages end differ: whole warps for the tensor-memory instructions behind
+        };
+        // The keys go into the group's TMEM buffer one own tile ahead, so the
+        // scores are there when the tile's turn comes.
+        auto unpack_keys = [&]() {
+            uint4 codes[D / 32];
+            uint32_t sc[D / 64];
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) sc[c] = *reinterpret_cast<const uint32_t *>(kscale + c * 4);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) codes[c] = *reinterpret_cast<const uint4 *>(kraw + c * (kTile * 16));
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[16];
+                if (c & 1) unpack32(codes[c], scale_f16x2<2>(sc[c / 2]), scale_f16x2<3>(sc[c / 2]), r);
+                else unpack32(codes[c], scale_f16x2<0>(sc[c / 2]), scale_f16x2<1>(sc[c / 2]), r);
+                tmem_st16(tm + lane_base + kColK + sg * 64 + c * 16, r);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.k_full[sg]);
+        };
+        unsigned long long rec = find(sg), next = 0;   // records of this tile; of the own tile behind it
+        copy(rec, kraw, kscale);
+        copy(rec ? rec + hb : 0, vraw, vscale);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (sg < tiles) unpack_keys();
+        next = find(sg + kGroups);
+        copy(next, kraw, kscale);
+        if (sg == 0) {
             uint32_t one[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) one[i] = 0x3c003c00u;
             tmem_st16(tm + lane_base + kColOne, one);
         }
-        for (; g < tiles; ++g) {
-                const int st = g % S, bb = g & 1;
-                wait(&ms.raw_full[st], (g / S) & 1, abort, a.budget);
-                wait(&ms.s_full[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
-                tc_fence_after();
-                const uint8_t *raw = sm + Y::raw + st * Y::kRec;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; c += 2) {   // 64 dims: two pieces of codes, one word of scales
-                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(raw + soff + c * 2);
-                    const uint4 c0 = *reinterpret_cast<const uint4 *>(raw + koff + c * a.P * 16);
-                    const uint4 c1 = *reinterpret_cast<const uint4 *>(raw + koff + (c + 1) * a.P * 16);
-                    uint32_t r[16];
-                    unpack32(c0, scale_f16x2<0>(sc), scale_f16x2<1>(sc), r);
-                    tmem_st16(tm + lane_base + kColK + bb * 64 + c * 16, r);
-                    unpack32(c1, scale_f16x2<2>(sc), scale_f16x2<3>(sc), r);
-                    tmem_st16(tm + lane_base + kColK + bb * 64 + c * 16 + 16, r);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ms.k_full[bb]);
-                    mbar_arrive(&ms.raw_empty[st]);
-                }
-        }
-    } else if (warp < 8) {
-        // -------------------------------------------------------- values
-        const int key = tid - 128, R = record_bytes(a.P, D);
-        const int half = half_bytes(a.P, D);
-        const int voff = key / a.P * R + half + key % a.P * 16;
-        const int soff = key / a.P * R + half + half_scales_off(a.P, D) + key % a.P * (D / 16);
-        for (; g < tiles; ++g) {
-                const int st = g % S, bb = g & 1;
-                wait(&ms.raw_full[st], (g / S) & 1, abort, a.budget);
-                wait(&ms.pv_done[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
-                const uint8_t *raw = sm + Y::raw + st * Y::kRec;
-                uint8_t *vrow = sm + Y::v + bb * Y::kVBytes + key * 128;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; c += 2) {
-                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(raw + soff + c * 2);
-                    const uint4 c0 = *reinterpret_cast<const uint4 *>(raw + voff + c * a.P * 16);
-                    const uint4 c1 = *reinterpret_cast<const uint4 *>(raw + voff + (c + 1) * a.P * 16);
-                    uint32_t r[16];
-                    unpack32(c0, scale_f16x2<0>(sc), scale_f16x2<1>(sc), r);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        *reinterpret_cast<uint4 *>(vrow + (u ^ (key & 7)) * 16) =
-                            make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
-                    unpack32(c1, scale_f16x2<2>(sc), scale_f16x2<3>(sc), r);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        *reinterpret_cast<uint4 *>(vrow + ((4 + u) ^ (key & 7)) * 16) =
-                            make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
-                    vrow += kTile * 128;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ms.v_full[bb]);
-                    mbar_arrive(&ms.raw_empty[st]);
-                }
-        }
-    } else if (warp < 12) {
-        // ------------------------------------------------------- softmax
-        const int key = tid - 256, sw = warp - 8;
-        const uint32_t lane_base = (uint32_t)(sw * 32) << 16;
-        if (key == 0) a.desc[blockIdx.x * kDescInts] = 0;
-        int piece = 0;
-        do {
+        // The group of tile g - 1, and its parity when this group's is even.
+        const int p1 = (sg + kGroups - 1) % kGroups;
+        const uint32_t x1 = sg < 1;
+        uint32_t ph = 0;       // parity of this group's barriers for its current tile
+        int end = 0;           // the piece's tiles are [.., end) of the run
+        g = sg;
+        for (int piece = 0; end < tiles; ++piece) {
             Rows &rw = ms.rows[piece & 1];
             wait(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
-            if (soft_any(*abort != 0)) break;   // the piece may not be there: the four warps leave together
-            const int nr = rw.nr, N = (nr + 15) / 16 * 16, t0 = rw.t0, t1 = rw.t1;
+            if (soft_any(sg, *abort != 0)) break;   // the piece may not be there: the four warps leave together
+            const int nr = rw.nr, N = (nr + 15) / 16 * 16, t0 = rw.t0, t1 = rw.t1, g0 = end;
             // Tiles that every row sees whole need no mask.
             const int all_hi = rw.lim[0].y, all_lo = rw.lim[nr - 1].x;
-            for (int t = t0; t < t1; ++t, ++g) {
-                const int bb = g & 1;
-                const int kpos = rw.base + t * kTile;
+            int version = 0;
+            end += t1 - t0;
+            for (; g < end; g += kGroups) {
+                const int t = t0 + g - g0;
+                const int ri = g % kRing, kpos = rw.base + t * kTile, me = kpos + key;
+                const uint32_t rp = (g / kRing) & 1;           // parity of the ring's barriers for this tile
+                const uint32_t ts = tm + lane_base + kColS + ri * kRows;
+                uint8_t *prow = sm + Y::p + ri * Y::kPBytes + key * 128;
                 const bool masked = kpos + kTile > all_hi || kpos < all_lo;
-                const int me = kpos + key;
-                uint8_t *prow = sm + Y::p + bb * Y::kPBytes + key * 128;
-                const uint32_t ts = tm + lane_base + kColS + bb * 64;
-                wait(&ms.s_full[bb], (g >> 1) & 1, abort, a.budget);
-                wait(&ms.pv_done[bb], ((g >> 1) & 1) ^ 1, abort, a.budget);
+                // Probabilities.
+                wait(&ms.pv_done[ri], rp ^ 1, abort, a.budget);      // of tile g - kRing: it read this P buffer
+                wait(&ms.s_full[sg], ph, abort, a.budget);
                 tc_fence_after();
-                bool raise = t == t0;
+                if (t == t0) {
+                    // The rows' first maxima: a quarter of the rows a warp, over
+                    // its own 32 keys.  Any key's score will do -- P of the key
+                    // that set it is 1, and a tile that passes it by too much raises it.
+#pragma unroll 1
+                    for (int r0 = sw * (N / 4); r0 < (sw + 1) * (N / 4); r0 += 4) {
+                        __syncwarp();
+                        uint32_t s[4];
+                        tmem_ld4(ts + r0, s);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x = __uint_as_float(s[i]) * rw.mul(r0 + i);
+                            if (masked) {
+                                const int2 l = rw.lim[r0 + i];
+                                if (me < l.x || me >= l.y) x = -INFINITY;
+                            }
+                            x = warp_max_f32(x);
+                            if (lane == 0) rw.neg_max(r0 + i) = x == x ? -x : INFINITY;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.m_full[piece & 1]);
+                }
+                if (t < t0 + kGroups) wait(&ms.m_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
+                bool raise = false, mine = t == t0, have_v = false;   // mine: tile g - 1 had its turn (or is another item's)
                 for (;;) {
                     if (raise) {
                         // New maxima over the tile: a warp's 32 keys, then the four warps.
 #pragma unroll 1
                         for (int r0 = 0; r0 < N; r0 += 4) {
+                            __syncwarp();
                             uint32_t s[4];
                             tmem_ld4(ts + r0, s);
                             tmem_ld_wait();
@@ -525,20 +595,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                                 x[i] = warp_max_f32(x[i]);
                             }
                             if (lane == 0)
-                                *reinterpret_cast<float4 *>(&ms.wmax[sw][r0]) = make_float4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<float4 *>(&ms.wmax[sg][sw][r0]) = make_float4(x[0], x[1], x[2], x[3]);
                         }
-                        soft_sync();
+                        soft_sync(sg);
                         if (key < N) {
                             float &neg = rw.neg_max(key);
                             const float old = -neg;
-                            const float nm = fmaxf(fmaxf(fmaxf(ms.wmax[0][key], ms.wmax[1][key]),
-                                                         fmaxf(ms.wmax[2][key], ms.wmax[3][key])), old);
-                            ms.fac[key] = nm == old ? 1.f : fast_exp2(old - nm);
+                            const float nm = fmaxf(fmaxf(fmaxf(ms.wmax[sg][0][key], ms.wmax[sg][1][key]),
+                                                         fmaxf(ms.wmax[sg][2][key], ms.wmax[sg][3][key])), old);
+                            ms.fac[sg][key] = nm == old ? 1.f : fast_exp2(old - nm);
                             neg = -nm;
                         }
-                        soft_sync();
+                        if (key == 0) ++rw.version;
+                        ++version;
+                        soft_sync(sg);
                         if (t > t0) {
-                            wait(&ms.pv_done[bb ^ 1], ((g - 1) >> 1) & 1, abort, a.budget);
+                            wait(&ms.pv_done[(g - 1) % kRing], ((g - 1) / kRing) & 1, abort, a.budget);
                             tc_fence_after();
 #pragma unroll 1
                             for (int r0 = 0; r0 < N; r0 += 4) {
@@ -548,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    const float f = ms.fac[r0 + i];
+                                    const float f = ms.fac[sg][r0 + i];
                                     o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                                     l[i] = __float_as_uint(__uint_as_float(l[i]) * f);
                                 }
@@ -558,157 +630,205 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                             tmem_st_wait();
                         }
                     }
-                    float top;
+                    float top = -INFINITY;
                     if (masked) {   // rare: one code for every number of rows
-                        top = -INFINITY;
                         for (int c = 0; c < N; c += 16)
                             top = fmaxf(top, probs<1, true>(ts, rw, prow, c, key, me));
-                    } else if (N == 16) {
-                        top = probs<1, false>(ts, rw, prow, 0, key, me);
-                    } else if (N == 32) {
-                        top = probs<2, false>(ts, rw, prow, 0, key, me);
-                    } else if (N == 48) {
-                        top = probs<3, false>(ts, rw, prow, 0, key, me);
                     } else {
-                        top = probs<4, false>(ts, rw, prow, 0, key, me);
+                        if (N == 16) top = probs<1, false>(ts, rw, prow, 0, key, me);
+                        else if (N == 32) top = probs<2, false>(ts, rw, prow, 0, key, me);
+                        else top = probs<3, false>(ts, rw, prow, 0, key, me);
                     }
-                    if (raise) break;                       // at most one raise a tile
-                    raise = soft_any(top > kRaise);
+                    if (!have_v) {
+                        have_v = true;
+                        // The next own tile's keys: the scores of this tile have read the buffer.
+                        // (Both copies were asked for an own tile ago.)
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        if (g + kGroups < tiles) unpack_keys();
+                        const unsigned long long after = find(g + 2 * kGroups);
+                        copy(after, kraw, kscale);
+                        // Values.  Their buffer was last read by the products of tile g - 2.
+                        uint8_t *vrow = sm + Y::v + (g & 1) * Y::kVBytes + key * 128;
+                        uint4 codes[D / 32];
+                        uint32_t sc[D / 64];
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) sc[c] = *reinterpret_cast<const uint32_t *>(vscale + c * 4);
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c)
+                            codes[c] = *reinterpret_cast<const uint4 *>(vraw + c * (kTile * 16));
+                        if (g >= 2) wait(&ms.pv_done[(g - 2) % kRing], ((g - 2) / kRing) & 1, abort, a.budget);
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t r[16];
+                            if (c & 1) unpack32(codes[c], scale_f16x2<2>(sc[c / 2]), scale_f16x2<3>(sc[c / 2]), r);
+                            else unpack32(codes[c], scale_f16x2<0>(sc[c / 2]), scale_f16x2<1>(sc[c / 2]), r);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                *reinterpret_cast<uint4 *>(vrow + (c / 2) * (kTile * 128) +
+                                                           (((c & 1) * 4 + u) ^ (key & 7)) * 16) =
+                                    make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+                        }
+                        rec = next;
+                        next = after;
+                        copy(rec ? rec + hb : 0, vraw, vscale);
+                    }
+                    if (!mine) {
+                        mine = true;
+                        wait(&ms.turn[p1], ph ^ x1, abort, a.budget);
+                        const int v = __shfl_sync(0xffffffffu, rw.version, 0);
+                        if (v != version) {
+                            version = v;
+                            continue;
+                        }
+                    }
+                    if (raise) break;                  // at most one raise a tile
+                    raise = soft_any(sg, top > kRaise);
                     if (!raise) break;
                 }
+                if (t == t0 && g > 0) wait(&ms.turn[p1], ph ^ x1, abort, a.budget);   // the last item's O was read
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_full[bb]);
-            }
-            // The piece's result: this thread's dim of every row.
-            wait(&ms.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, a.budget);
-            tc_fence_after();
-            const bool whole = t0 == 0 && t1 == rw.nt;
-            const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+                if (lane == 0) mbar_arrive(&ms.vp_full[ri]);
+                if (t + 1 == t1) {
+                    // The piece's result: this thread's dim of every row.
+                    wait(&ms.pv_done[ri], rp, abort, a.budget);
+                    tc_fence_after();
+                    const bool whole = t0 == 0 && t1 == rw.nt;
+                    const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
 #pragma unroll 1
-            for (int r0 = 0; r0 < nr; r0 += 4) {   // a short loop: code that runs once an item is fetched anew each time
-                uint32_t o[4], l[4];
-                tmem_ld4(tm + lane_base + kColO + r0, o);
-                tmem_ld4(tm + lane_base + kColL + r0, l);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + i;
-                    const float oo = __uint_as_float(o[i]), ll = __uint_as_float(l[i]);
-                    if (r < nr && key < D) {
+                    for (int r0 = 0; r0 < nr; r0 += 16) {
+                        __syncwarp();
+                        uint32_t o[16], l[16];
+                        tmem_ld16(tm + lane_base + kColO + r0, o);
+                        tmem_ld16(tm + lane_base + kColL + r0, l);
+                        tmem_ld_wait();
                         if (whole) {
-                            const float y = ll == 0.f ? 0.f : oo * __fdividef(a.v_mul, ll);
-                            a.out[(long long)rw.orow[r] * D + key] = __float2bfloat16_rn(y);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                // No visible key: the sum is 0 and so is O.
+                                const float ll = __uint_as_float(l[i]), inv = ll == 0.f ? 0.f : rcp(ll) * a.v_mul;
+                                const float y = __uint_as_float(o[i]) * inv;
+                                if (r0 + i < nr && key < D)
+                                    a.out[(long long)rw.orow[r0 + i] * D + key] = __float2bfloat16_rn(y);
+                            }
                         } else {
-                            a.part_o[((size_t)slot * kRows + r) * D + key] = oo;
-                            if (key == 0) a.part_ml[slot * kRows + r] = make_float2(-rw.neg_max(r), ll);
+                            float *po = a.part_o + ((size_t)slot * kRows + r0) * D + key;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (r0 + i < nr && key < D) po[i * D] = __uint_as_float(o[i]);
+                                if (r0 + i < nr && key == i)
+                                    a.part_ml[slot * kRows + r0 + i] =
+                                        make_float2(-rw.neg_max(r0 + i), __uint_as_float(l[i]));
+                            }
                         }
                     }
+                    if (!whole && t0 == 0 && key == 0) {
+                        int32_t *d = a.desc + blockIdx.x * kDescInts;
+                        d[1] = rw.q0;
+                        d[2] = rw.r0;
+                        d[3] = nr;
+                        d[4] = rw.h;
+                        d[5] = quota;
+                        d[0] = rw.nt - t1;
+                    }
+                    tc_fence_before();
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.turn[sg]);
+                ph ^= 1;
             }
-            if (!whole && t0 == 0 && key == 0) {
-                int32_t *d = a.desc + blockIdx.x * kDescInts;
-                d[1] = rw.q0;
-                d[2] = rw.r0;
-                d[3] = nr;
-                d[4] = rw.h;
-                d[5] = quota;
-                d[0] = rw.nt - t1;
-            }
-            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.q_empty[piece & 1]);
-            ++piece;
-        } while (g < tiles);
-    } else if (warp == 12) {
-        // ------------------------------------------------------ producer
-        const uint64_t pol = policy_evict_first();
-        const int R = record_bytes(a.P, D), ppt = kTile / a.P;
+        }
+    } else if (warp == kWarpLoad) {
+        // --------------------------------------------------------- pages
+        // A lane per page of a tile: its record's address, up to kAhead tiles
+        // before they are used.
+        const int ppt = kTile / a.P;
+        const unsigned long long rec_bytes = record_bytes(a.P, D);
         Walk wk(a, prefix, w0, w1);
-        do {
-            for (int t = wk.t0; t < wk.t1; ++t, ++g) {
-                const int st = g % S;
-                const int key0 = wk.k.base + t * kTile;
-                const int np = min(ppt, max(0, (wk.k.hi - key0 + a.P - 1) / a.P));
-                int page = 0;
-                if (lane < np) {
-                    page = __ldg(a.table + (long long)wk.b * a.max_pages + key0 / a.P + lane);
-                    if (page < 0 || page >= a.n_pages) {
-                        flag_status(a.hdr, DSPARK_DEV_PAGE_RANGE);
-                        page = 0;
-                    }
+        for (int t = wk.t0; g < tiles; ++g) {
+            const int key0 = wk.k.base + t * kTile, np = min(ppt, max(0, (wk.k.hi - key0 + a.P - 1) / a.P));
+            unsigned long long rec = 0;
+            if (lane < np) {
+                int page = __ldg(a.table + (long long)wk.b * a.max_pages + key0 / a.P + lane);
+                if (page < 0 || page >= a.n_pages) {
+                    flag_status(a.hdr, DSPARK_DEV_PAGE_RANGE);
+                    page = 0;
                 }
-                wait(&ms.raw_empty[st], ((g / S) & 1) ^ 1, abort, a.budget);
-                const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
-                if (go) {
-                    if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], (uint32_t)(np * R));
-                    __syncwarp();
-                    if (lane < np)
-                        bulk_load(sm + Y::raw + st * Y::kRec + lane * R,
-                                  a.cache + ((size_t)page * a.Hkv + wk.h) * R, (uint32_t)R, &ms.raw_full[st], pol);
-                    issued = g + 1;
-                }
+                rec = reinterpret_cast<unsigned long long>(a.cache) +
+                      ((unsigned long long)page * a.Hkv + wk.h) * rec_bytes;
             }
-        } while (wk.next());
-    } else if (warp == 13) {
-        // ----------------------------------------------------------- MMA
-        int piece = 0;
-        // D = 64: the second 64 rows of the value operand repeat the first (their lanes are not read).
-        const uint32_t v0 = desc_lo(smem_u32(sm + Y::v), D == 128 ? kTile * 128 : 0);
-        const uint32_t p0 = desc_lo(smem_u32(sm + Y::p), 0), q0 = desc_lo(smem_u32(sm + Y::q), 16);
-        do {
-            wait(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
-            if (__shfl_sync(0xffffffffu, *abort, 0)) break;
-            const Rows &rw = ms.rows[piece & 1];
-            const int N = (rw.nr + 15) / 16 * 16, g_end = g + rw.t1 - rw.t0;
-            const uint32_t id_s = idesc_f16(N, false, false), id_o = idesc_f16(N, true, true),
-                           id_l = idesc_f16(N, false, true);
-            const uint32_t q_lo = q0 + (piece & 1) * (Y::kQBytes / 16);
-            ++piece;
-            bool first = true;
-            // One step ahead with the scores: step x issues the scores of tile x and the values of tile x - 1.
-            for (int x = g; x <= g_end; ++x) {
-                if (x < g_end) {
-                    const int bb = x & 1;
-                    wait(&ms.k_full[bb], (x >> 1) & 1, abort, a.budget);
+            const int st = g % kAhead;
+            if (!__all_sync(0xffffffffu, wait1(&ms.rec_empty[st], ((g / kAhead) & 1) ^ 1, abort, a.budget))) break;
+            if (lane < 8) ms.rec[st][lane] = rec;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.rec_full[st]);
+            if (++t == wk.t1 && wk.next()) t = wk.t0;
+        }
+    } else if (warp == kWarpQk) {
+        // -------------------------------------------------------- scores
+        if (elect_one()) {
+            const uint32_t q0 = desc_lo(smem_u32(sm + Y::q), 16);
+            for (int piece = 0; g < tiles; ++piece) {
+                if (!wait1(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget)) break;
+                const Rows &rw = ms.rows[piece & 1];
+                const int g_end = g + rw.t1 - rw.t0;
+                const uint32_t id = idesc_f16((rw.nr + 15) / 16 * 16, false, false);
+                const uint32_t q_lo = q0 + (piece & 1) * (Y::kQBytes / 16);
+                bool ok = true;
+                for (; g < g_end; ++g) {
+                    const int sg = g % kGroups, ri = g % kRing;
+                    // The keys are there, and the scores of tile g - kRing are done with.
+                    ok = wait1(&ms.k_full[sg], (g / kGroups) & 1, abort, a.budget) &&
+                         wait1(&ms.vp_full[ri], ((g / kRing) & 1) ^ 1, abort, a.budget);
+                    if (!ok) break;
                     tc_fence_after();
-                    const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
-                    if (go && elect_one()) {
-                        const uint32_t ds = tm + kColS + bb * 64, dk = tm + kColK + bb * 64;
-                        mma_ts<false>(ds, dk, q_lo, id_s);
+                    const uint32_t ds = tm + kColS + ri * kRows, dk = tm + kColK + sg * 64;
+                    mma_ts<false>(ds, dk, q_lo, id);
 #pragma unroll
-                        for (int kk = 1; kk < D / 16; ++kk)
-                            mma_ts<true>(ds, dk + kk * 8, q_lo + (kk / 4) * (kRows * 8) + (kk & 3) * 2, id_s);
-                        mma_commit(&ms.s_full[bb]);
-                    }
-                    __syncwarp();
+                    for (int kk = 1; kk < D / 16; ++kk)
+                        mma_ts<true>(ds, dk + kk * 8, q_lo + (kk / 4) * (kRows * 8) + (kk & 3) * 2, id);
+                    mma_commit(&ms.s_full[sg]);
                 }
-                if (x > g) {
-                    const int bb = (x - 1) & 1, ph = ((x - 1) >> 1) & 1;
-                    wait(&ms.v_full[bb], ph, abort, a.budget);
-                    wait(&ms.p_full[bb], ph, abort, a.budget);
-                    tc_fence_after();
-                    const int go = __shfl_sync(0xffffffffu, *abort == 0, 0);
-                    if (go && elect_one()) {
-                        const uint32_t v_lo = v0 + bb * (Y::kVBytes / 16), p_lo = p0 + bb * (Y::kPBytes / 16);
-                        if (first)
-                            mma_values<true>(tm, v_lo, p_lo, id_o, id_l);
-                        else
-                            mma_values<false>(tm, v_lo, p_lo, id_o, id_l);
-                        mma_commit(&ms.pv_done[bb]);
-                    }
-                    __syncwarp();
-                    first = false;
-                }
+                if (!ok) break;
             }
-            g = g_end;
-        } while (g < tiles);
+        }
+    } else if (warp == kWarpPv) {
+        // -------------------------------------------------------- values
+        // D = 64: the second 64 rows of the value operand repeat the first (their lanes are not read).
+        if (elect_one()) {
+            const uint32_t v0 = desc_lo(smem_u32(sm + Y::v), D == 128 ? kTile * 128 : 0);
+            const uint32_t p0 = desc_lo(smem_u32(sm + Y::p), 0);
+            for (int piece = 0; g < tiles; ++piece) {
+                if (!wait1(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget)) break;
+                const Rows &rw = ms.rows[piece & 1];
+                const int N = (rw.nr + 15) / 16 * 16, g0 = g, g_end = g + rw.t1 - rw.t0;
+                const uint32_t id_o = idesc_f16(N, true, true), id_l = idesc_f16(N, false, true);
+                bool ok = true;
+                for (; g < g_end; ++g) {
+                    const int ri = g % kRing;
+                    ok = wait1(&ms.vp_full[ri], (g / kRing) & 1, abort, a.budget);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t v_lo = v0 + (g & 1) * (Y::kVBytes / 16), p_lo = p0 + ri * (Y::kPBytes / 16);
+                    if (g == g0)
+                        mma_values<true>(tm, v_lo, p_lo, id_o, id_l);
+                    else
+                        mma_values<false>(tm, v_lo, p_lo, id_o, id_l);
+                    mma_commit(&ms.pv_done[ri]);
+                }
+                if (!ok) break;
+            }
+        }
     } else {
         // ------------------------------------------------------- queries
-        // D / 8 lanes a row; scaled by a power of two so that f16 holds them exactly.
-        constexpr int kLanes = D / 8, kPass = 64 / kLanes, kBatch = 4;
-        const int id = tid - 14 * 32, part = id % kLanes;
+        // A lane works out where rows lane and lane + 32 come from and what they
+        // see; then D / 16 lanes a row, 16 dims each, scale it by a power of two
+        // so that f16 holds it exactly.
+        constexpr int kLanes = D / 16, kPass = 32 / kLanes, kBatch = 2;
+        const int part = lane % kLanes, rsub = lane / kLanes;
         int piece = 0;
         Walk wk(a, prefix, w0, w1);
         do {
@@ -716,7 +836,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
             uint8_t *qs = sm + Y::q + (piece & 1) * Y::kQBytes;
             const int nr = wk.k.nr, N = (nr + 15) / 16 * 16;
             wait(&ms.q_empty[piece & 1], ((piece >> 1) & 1) ^ 1, abort, a.budget);
-            if (id == 0) {
+            const __nv_bfloat16 *src[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = lane + 32 * u, gr = wk.k.r0 + min(r, nr - 1), j = gr / a.group;
+                const int hd = wk.h * a.group + gr - j * a.group, pos = wk.q.L - wk.q.n + j;
+                src[u] = a.q + (long long)(wk.q.q0 + j) * a.q_stride + hd * D;
+                if (r >= kRows) continue;
+                rw.lim[r] = r < nr ? make_int2(a.window > 0 ? max(0, pos - a.window + 1) : 0, pos + 1)
+                                   : make_int2(0, 0);
+                rw.orow[r] = (wk.q.q0 + j) * a.Hq + hd;
+            }
+            if (lane == 0) {
                 rw.nr = nr;
                 rw.base = wk.k.base;
                 rw.t0 = wk.t0;
@@ -725,53 +856,53 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                 rw.q0 = wk.q.q0;
                 rw.r0 = wk.k.r0;
                 rw.h = wk.h;
+                rw.version = 0;
             }
 #pragma unroll 1
-            for (int rr = id / kLanes; rr < N; rr += kPass * kBatch) {
-                uint4 w[kBatch];
-                int j[kBatch], hd[kBatch];
+            for (int rr = 0; rr < N; rr += kPass * kBatch) {   // N is a multiple of 16, as is the step (or half of it)
+                uint4 w[kBatch][2];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const int r = rr + u * kPass, gr = wk.k.r0 + r;
-                    j[u] = gr / a.group;
-                    hd[u] = wk.h * a.group + gr - j[u] * a.group;
-                    w[u] = make_uint4(0, 0, 0, 0);
-                    if (r < nr)
-                        w[u] = __ldg(reinterpret_cast<const uint4 *>(a.q + (long long)(wk.q.q0 + j[u]) * a.q_stride +
-                                                                     hd[u] * D + part * 8));
+                    const int r = rr + u * kPass + rsub;
+                    const unsigned long long p0 = __shfl_sync(0xffffffffu, (unsigned long long)src[0], r & 31);
+                    const unsigned long long p1 = __shfl_sync(0xffffffffu, (unsigned long long)src[1], r & 31);
+                    const uint4 *p = reinterpret_cast<const uint4 *>(r < 32 ? p0 : p1) + part * 2;
+                    w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
+                    if (r < nr) {
+                        w[u][0] = __ldg(p);
+                        w[u][1] = __ldg(p + 1);
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const int r = rr + u * kPass;
-                    if (r >= N) continue;   // N is a multiple of 16: whole warps
-                    const float f[8] = {bf16lo(w[u].x), bf16hi(w[u].x), bf16lo(w[u].y), bf16hi(w[u].y),
-                                        bf16lo(w[u].z), bf16hi(w[u].z), bf16lo(w[u].w), bf16hi(w[u].w)};
-                    float mx = 0.f;
+                    const int r = rr + u * kPass + rsub;
+                    const uint32_t v[8] = {w[u][0].x, w[u][0].y, w[u][0].z, w[u][0].w,
+                                           w[u][1].x, w[u][1].y, w[u][1].z, w[u][1].w};
+                    uint32_t top = 0;   // magnitudes of bf16 pairs as integers: order as the values
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[i]));
+                    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
+                    top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // 2^e * max in [2^14, 2^15); e within fp32's exponents.
-                    const int ex = (int)(__float_as_uint(mx) >> 23) - 127;
-                    const int e = (mx > 0.f && ex < 128) ? min(14 - ex, 100) : 0;
+                    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // 2^e * max in [2^14, 2^15); e within fp32's exponents; infinities and NaN stay.
+                    const int ex = (int)(top >> 7) - 127;
+                    const int e = (top > 0 && ex < 128) ? min(14 - ex, 100) : 0;
                     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    uint32_t hh[4];
+                    uint32_t hh[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __half2 x = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+                    for (int i = 0; i < 8; ++i) {
+                        const __half2 x = __floats2half2_rn(bf16lo(v[i]) * up, bf16hi(v[i]) * up);
                         hh[i] = *reinterpret_cast<const uint32_t *>(&x);
                     }
-                    *reinterpret_cast<uint4 *>(qs + (part / 8) * (kRows * 128) + r * 128 +
-                                               (((part & 7) ^ (r & 7)) * 16)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-                    if (part == 0) {
-                        const bool live = r < nr;
-                        const int pos = wk.q.L - wk.q.n + j[u];
-                        rw.mul(r) = live ? a.qk_mul * down : 0.f;
-                        rw.neg_max(r) = live ? INFINITY : 0.f;
-                        rw.lim[r] = live ? make_int2(a.window > 0 ? max(0, pos - a.window + 1) : 0, pos + 1)
-                                         : make_int2(0, 0);
-                        rw.orow[r] = (wk.q.q0 + j[u]) * a.Hq + hd[u];
+                    if (r < N) {
+                        uint8_t *row = qs + (part / 4) * (kRows * 128) + r * 128;
+                        const int c = part % 4 * 2;
+                        *reinterpret_cast<uint4 *>(row + (c ^ (r & 7)) * 16) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                        *reinterpret_cast<uint4 *>(row + ((c + 1) ^ (r & 7)) * 16) = make_uint4(hh[4], hh[5], hh[6], hh[7]);
+                        if (part == 0) {
+                            rw.mul(r) = r < nr ? a.qk_mul * __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+                            rw.neg_max(r) = r < nr ? INFINITY : 0.f;
+                        }
                     }
                 }
             }
@@ -788,14 +919,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     __syncthreads();
     if (*abort) {
         int own = 0;
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (tid == 0) flag_status(a.hdr, DSPARK_DEV_TIMEOUT);
-        if (warp == 12) {
-            for (int u = max(0, issued - S); u < issued; ++u)
-                mbar_wait_bounded(&ms.raw_full[u % S], (u / S) & 1, &own, kWaitBudget);
-        } else if (warp == 13) {
-            if (elect_one()) mma_commit(&ms.drain);
+        if (warp == kWarpQk || warp == kWarpPv) {
+            uint64_t *bar = &ms.drain[warp - kWarpQk];
+            if (elect_one()) mma_commit(bar);
             __syncwarp();
-            mbar_wait_bounded(&ms.drain, 0, &own, kWaitBudget);
+            mbar_wait_bounded(bar, 0, &own, kWaitBudget);
         }
         __syncthreads();
     }
@@ -842,7 +972,9 @@ __global__ void __launch_bounds__(256) cache_attention_join(const AttnArgs a) {
 
 template <int D>
 cudaError_t launch_d(const AttnArgs &a, int grid, cudaStream_t st) {
-    const size_t bytes = Lay<D>::misc + (sizeof(Misc) + 15) / 16 * 16 + (size_t)(a.B + 1) * 4 + 1024;
+    const size_t bytes = Lay<D>::misc + sizeof(Misc) + 1024;
+    static_assert(Lay<D>::misc + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory of an SM");
+    static_assert(4096 * sizeof(int) <= kRing * Lay<D>::kPBytes, "the prefix of the largest batch");
     cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)bytes);
     if (e != cudaSuccess) return e;
