@@ -310,55 +310,72 @@ def dspark_gather_admitted_targets(Tlog_host, Tlog_dev, ell, stream=None):
           G1 - 1, V, _dtype(Tlog_dev), _stream(stream))
 
 
-def _rows(t, what):
+# The calls of the target pass run once per layer and round, so their
+# marshalling is kept short: plain integers for pointers, the raw stream, and
+# one device comparison per tensor.
+def _device_of(t):
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("libdspark takes device tensors")
+    return d
+
+
+def _dense(t, dev):
+    """Pointer of a contiguous tensor on device `dev` (None passes)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"libdspark takes tensors of one device: {t.device} and cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError("libdspark takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _ints(t, dev, n, what):
+    """Pointer of an int32 tensor of at least n elements."""
+    if t.dtype is not torch.int32 or t.numel() < n:
+        raise ValueError(f"{what}: an int32 tensor of at least {n} elements, got {t.dtype} of {t.numel()}")
+    return _dense(t, dev)
+
+
+def _rows(t, dev, what):
     """(pointer, token stride) of a [T, H, D] device tensor whose heads are dense; the tokens may lie apart (a
     slice of a fused projection)."""
-    if not t.is_cuda:
-        raise ValueError("libdspark takes device tensors")
+    if t.get_device() != dev:
+        raise ValueError(f"libdspark takes tensors of one device: {t.device} and cuda:{dev}")
     T, H, D = t.shape
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != D):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
         raise ValueError(f"{what}: the heads of a token must be dense")
-    return ctypes.c_void_p(t.data_ptr()), (s[0] if T > 1 else max(s[0], H * D))
+    return t.data_ptr(), (s0 if T > 1 else max(s0, H * D))
 
 
-def _ints(n, what, *tensors):
-    for t in tensors:
-        if t.dtype != torch.int32 or t.numel() < n:
-            raise ValueError(f"{what}: int32 tensors of at least {n} elements, got {t.dtype} of {t.numel()}")
-
-
-def _launch(fn, t, stream, *args):
-    """Call `fn` with the stream of t's device appended, on that device (which need not be the current one)."""
-    if t.device.index == torch.cuda.current_device():
-        _call(fn, *args, _stream(stream))
+def _launch(fn, dev, stream, *args):
+    """Call `fn` with the stream appended, on device `dev` (which need not be the current one)."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    f = getattr(_lib or load(), fn)
+    if dev == torch._C._cuda_getDevice():
+        st = f(*args, raw)
     else:
-        with torch.cuda.device(t.device):
-            _call(fn, *args, _stream(stream))
-
-
-def _same_device(*tensors):
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}")
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    if st != 0:
+        raise DsparkError(fn, st)
 
 
 def _cache_dims(cache, page, D):
     """(n_pages, Hkv) of a cache tensor [n_pages, Hkv, record bytes]."""
+    shape = cache.shape
     need = dspark_cache_record_bytes(page, D)
-    if cache.dtype != torch.uint8 or cache.dim() != 3 or need == 0 or cache.shape[2] != need:
+    if cache.dtype is not torch.uint8 or len(shape) != 3 or need == 0 or shape[2] != need:
         raise ValueError(f"cache: uint8 [n_pages, Hkv, {need}] for pages of {page} tokens and heads of {D}, got "
-                         f"{cache.dtype} {tuple(cache.shape)}")
-    return cache.shape[0], cache.shape[1]
+                         f"{cache.dtype} {tuple(shape)}")
+    return shape[0], shape[1]
 
 
 def dspark_cache_record_bytes(page, D) -> int:
     """Bytes of one (page, head) record of the 4-bit cache; 0 for an unsupported page size or head dim."""
-    return int(load().dspark_cache_record_bytes(page, D))
+    return (_lib or load()).dspark_cache_record_bytes(page, D)
 
 
 def dspark_cache_plan(ctx, ell, G, table, held, free_list, free_count, page, ws, q_start_out, kv_len_out, slot_out,
@@ -367,15 +384,14 @@ def dspark_cache_plan(ctx, ell, G, table, held, free_list, free_count, page, ws,
     ctx [B] and admitted lengths ell [B]; table [B, max_pages], held [B] and
     free_count [1] are updated, free_list [n_pages] is read.  slot_out and
     pos_out hold B * (G + 1) entries, -1 behind the last row."""
+    dev = _device_of(table)
     B, max_pages = table.shape
-    _ints(B, "ctx, ell, held, kv_len_out", ctx, ell, held, kv_len_out)
-    _ints(B + 1, "q_start_out", q_start_out)
-    _ints(B * (G + 1), "slot_out, pos_out", slot_out, pos_out)
-    _ints(1, "table, free_list, free_count", table, free_list, free_count)
-    _same_device(ctx, ell, table, held, free_list, free_count, ws, q_start_out, kv_len_out, slot_out, pos_out)
-    _launch("dspark_cache_plan", table, stream, _ptr(ctx), _ptr(ell), B, int(G), int(page), max_pages,
-            free_list.numel(), _ptr(table), _ptr(held), _ptr(free_list), _ptr(free_count), _ptr(ws),
-            ws.numel() * ws.element_size(), _ptr(q_start_out), _ptr(kv_len_out), _ptr(slot_out), _ptr(pos_out))
+    T = B * (G + 1)
+    _launch("dspark_cache_plan", dev, stream, _ints(ctx, dev, B, "ctx"), _ints(ell, dev, B, "ell"), B, int(G),
+            int(page), max_pages, free_list.numel(), _ints(table, dev, 1, "table"), _ints(held, dev, B, "held"),
+            _ints(free_list, dev, 1, "free_list"), _ints(free_count, dev, 1, "free_count"), _dense(ws, dev),
+            ws.nbytes, _ints(q_start_out, dev, B + 1, "q_start_out"), _ints(kv_len_out, dev, B, "kv_len_out"),
+            _ints(slot_out, dev, T, "slot_out"), _ints(pos_out, dev, T, "pos_out"))
 
 
 def dspark_cache_commit(ctx, q_start, nout, done, table, held, free_list, free_count, page, ws, ctx_out,
@@ -383,16 +399,13 @@ def dspark_cache_commit(ctx, q_start, nout, done, table, held, free_list, free_c
     """After verification: ctx_out = ctx + nout (-1 where done [B], or None,
     is set), and the pages behind those tokens go back on the free list.
     ctx_out may be ctx."""
+    dev = _device_of(table)
     B, max_pages = table.shape
-    _ints(B, "ctx, nout, held, ctx_out", ctx, nout, held, ctx_out)
-    _ints(B + 1, "q_start", q_start)
-    _ints(1, "table, free_list, free_count", table, free_list, free_count)
-    if done is not None:
-        _ints(B, "done", done)
-    _same_device(ctx, q_start, nout, done, table, held, free_list, free_count, ws, ctx_out)
-    _launch("dspark_cache_commit", table, stream, _ptr(ctx), _ptr(q_start), _ptr(nout), _ptr(done), B, int(page),
-            max_pages, free_list.numel(), _ptr(table), _ptr(held), _ptr(free_list), _ptr(free_count), _ptr(ws),
-            ws.numel() * ws.element_size(), _ptr(ctx_out))
+    _launch("dspark_cache_commit", dev, stream, _ints(ctx, dev, B, "ctx"), _ints(q_start, dev, B + 1, "q_start"),
+            _ints(nout, dev, B, "nout"), None if done is None else _ints(done, dev, B, "done"), B, int(page),
+            max_pages, free_list.numel(), _ints(table, dev, 1, "table"), _ints(held, dev, B, "held"),
+            _ints(free_list, dev, 1, "free_list"), _ints(free_count, dev, 1, "free_count"), _dense(ws, dev),
+            ws.nbytes, _ints(ctx_out, dev, B, "ctx_out"))
 
 
 def dspark_qk_norm_rope(q, k, wq, wk, eps, pos, inv_freq, interleaved, n_rows, q_out, k_out, ws, v=None, cache=None,
@@ -401,51 +414,47 @@ def dspark_qk_norm_rope(q, k, wq, wk, eps, pos, inv_freq, interleaved, n_rows, q
     values into the 4-bit cache.  q [T, Hq, D], k and v [T, Hkv, D] may be
     slices of one projection; inv_freq [rot/2] f32 (None: no rotation); wq, wk
     [D] or None (no norm); n_rows: device int32 tensor or None."""
+    dev = _device_of(q)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
+    dt = q.dtype
     if k.shape != (T, Hkv, D) or q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
         raise ValueError("q, k, q_out and k_out differ in tokens, heads or dims")
     for t in (k, v, wq, wk, q_out, k_out):
-        if t is not None and t.dtype != q.dtype:
-            raise ValueError(f"one dtype for q, k, v, the weights and the outputs: {t.dtype} and {q.dtype}")
-    for w in (wq, wk):
-        if w is not None and w.numel() != D:
-            raise ValueError(f"norm weights have {D} elements")
+        if t is not None and t.dtype is not dt:
+            raise ValueError(f"one dtype for q, k, v, the weights and the outputs: {t.dtype} and {dt}")
+    if (wq is not None and wq.numel() != D) or (wk is not None and wk.numel() != D):
+        raise ValueError(f"norm weights have {D} elements")
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if rot:
-        if inv_freq.dtype != torch.float32:
-            raise ValueError("inv_freq is float32")
-        _ints(T, "pos", pos)
-    if n_rows is not None:
-        _ints(1, "n_rows", n_rows)
-    n_pages = 0
+    if rot and inv_freq.dtype is not torch.float32:
+        raise ValueError("inv_freq is float32")
+    n_pages, cp, sp, vp, vs = 0, None, None, None, 0
     if cache is not None:
         n_pages, heads = _cache_dims(cache, page, D)
         if v is None or slot is None or v.shape != k.shape or heads != Hkv:
             raise ValueError("a cache write needs v like k, slot, and a cache of k's heads")
-        _ints(T, "slot", slot)
-    _same_device(q, k, v, wq, wk, pos if rot else None, inv_freq, n_rows, q_out, k_out, ws, cache, slot)
-    qp, qs = _rows(q, "q")
-    kp, ks = _rows(k, "k")
-    vp, vs = (None, 0) if v is None else _rows(v, "v")
-    _launch("dspark_qk_norm_rope", q, stream, qp, qs, kp, ks, vp, vs, _ptr(wq), _ptr(wk), float(eps),
-            _ptr(pos) if rot else None, _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), _ptr(n_rows),
-            T, Hq, Hkv, D, _dtype(q), _ptr(q_out), _ptr(k_out), _ptr(cache), _ptr(slot), int(page), n_pages,
-            float(k_scale), float(v_scale), _ptr(ws), ws.numel() * ws.element_size())
+        cp, sp = _dense(cache, dev), _ints(slot, dev, T, "slot")
+        vp, vs = _rows(v, dev, "v")
+    qp, qs = _rows(q, dev, "q")
+    kp, ks = _rows(k, dev, "k")
+    _launch("dspark_qk_norm_rope", dev, stream, qp, qs, kp, ks, vp, vs, _dense(wq, dev), _dense(wk, dev), float(eps),
+            _ints(pos, dev, T, "pos") if rot else None, _dense(inv_freq, dev) if rot else None, rot,
+            1 if interleaved else 0, None if n_rows is None else _ints(n_rows, dev, 1, "n_rows"), T, Hq, Hkv, D,
+            _dtype(q), _dense(q_out, dev), _dense(k_out, dev), cp, sp, int(page), n_pages, float(k_scale),
+            float(v_scale), _dense(ws, dev), ws.nbytes)
 
 
 def dspark_cache_read(cache, slot, page, k_out, v_out, ws, k_scale=1.0, v_scale=1.0, stream=None):
     """Keys and values of the cached tokens slot [T] -> k_out, v_out
     [T, Hkv, D]; rows with a negative slot are left alone."""
+    dev = _device_of(cache)
     T, Hkv, D = k_out.shape
     n_pages, heads = _cache_dims(cache, page, D)
-    if v_out.shape != k_out.shape or v_out.dtype != k_out.dtype or heads != Hkv:
+    if v_out.shape != k_out.shape or v_out.dtype is not k_out.dtype or heads != Hkv:
         raise ValueError("k_out, v_out and the cache differ in heads, dims or dtype")
-    _ints(T, "slot", slot)
-    _same_device(cache, slot, k_out, v_out, ws)
-    _launch("dspark_cache_read", cache, stream, _ptr(cache), _ptr(slot), T, Hkv, D, int(page), n_pages,
-            float(k_scale), float(v_scale), _dtype(k_out), _ptr(k_out), _ptr(v_out), _ptr(ws),
-            ws.numel() * ws.element_size())
+    _launch("dspark_cache_read", dev, stream, _dense(cache, dev), _ints(slot, dev, T, "slot"), T, Hkv, D, int(page),
+            n_pages, float(k_scale), float(v_scale), _dtype(k_out), _dense(k_out, dev), _dense(v_out, dev),
+            _dense(ws, dev), ws.nbytes)
 
 
 def dspark_cache_attention_workspace_size(B, Hq, Hkv, D) -> int:
@@ -457,19 +466,17 @@ def dspark_cache_attention(q, cache, table, q_start, kv_len, page, scale, window
     """Attention of the round's rows q [T, Hq, D] (bf16) over the 4-bit cache:
     causal inside each request's block, the last `window` keys only when
     window > 0; table, q_start and kv_len as dspark_cache_plan leaves them."""
+    dev = _device_of(q)
     T, Hq, D = q.shape
     B, max_pages = table.shape
     n_pages, Hkv = _cache_dims(cache, page, D)
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("q and out differ in shape or dtype")
-    _ints(B + 1, "q_start", q_start)
-    _ints(B, "kv_len", kv_len)
-    _ints(1, "table", table)
-    _same_device(q, cache, table, q_start, kv_len, ws, out)
-    qp, qs = _rows(q, "q")
-    _launch("dspark_cache_attention", q, stream, qp, qs, _ptr(cache), _ptr(table), _ptr(q_start), _ptr(kv_len), B, T,
-            Hq, Hkv, D, int(page), max_pages, n_pages, float(scale), float(k_scale), float(v_scale), int(window),
-            _dtype(q), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out))
+    qp, qs = _rows(q, dev, "q")
+    _launch("dspark_cache_attention", dev, stream, qp, qs, _dense(cache, dev), _ints(table, dev, 1, "table"),
+            _ints(q_start, dev, B + 1, "q_start"), _ints(kv_len, dev, B, "kv_len"), B, T, Hq, Hkv, D, int(page),
+            max_pages, n_pages, float(scale), float(k_scale), float(v_scale), int(window), _dtype(q),
+            _dense(ws, dev), ws.nbytes, _dense(out, dev))
 
 
 def dspark_exp2_fma(x, y, stream=None):

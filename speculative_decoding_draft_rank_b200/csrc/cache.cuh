@@ -15,6 +15,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -52,6 +54,20 @@ __device__ __forceinline__ uint32_t scale_f16x2(uint32_t scales) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The dynamic shared memory limit of a kernel, set once per device (the call
+// costs about as much as a launch).  `done`: one word per kernel, a bit per
+// device; setting it twice does no harm.
+inline cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ------------------------------------------------------------------ plan

@@ -975,8 +975,8 @@ cudaError_t launch_d(const AttnArgs &a, int grid, cudaStream_t st) {
     const size_t bytes = Lay<D>::misc + sizeof(Misc) + 1024;
     static_assert(Lay<D>::misc + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory of an SM");
     static_assert(4096 * sizeof(int) <= kRing * Lay<D>::kPBytes, "the prefix of the largest batch");
-    cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(cache_attention_kernel<D>), bytes, done);
     if (e != cudaSuccess) return e;
     cache_attention_kernel<D><<<grid, kThreads, bytes, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -238,7 +238,8 @@ cudaError_t launch_cache_plan(const PlanArgs &a, cudaStream_t st) {
     // One CTA while its threads get a handful of tokens each, else a cluster of 8.
     const int ranks = a.B * (a.G + 1) <= 4 * kPlanThreads ? 1 : 8;
     const size_t bytes = (size_t)(3 * a.B + 3) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(cache_plan_kernel), (3 * 4096 + 3) * sizeof(int), done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks);
