@@ -96,8 +96,7 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
     if (dspark_status s = injected("dspark_cache_read")) return s;
     if (!dtype_ok(dtype)) return DSPARK_ERR_UNSUPPORTED_DTYPE;
     if (T < 0 || T > (1 << 24) || !heads_ok(Hkv, Hkv) || !cache_dim_ok(D) || !page_ok(P) || n_pages < 1 ||
-        (long long)n_pages * P > 0x7fffffffLL || !gain_ok(k_scale) || !gain_ok(v_scale) ||
-        (long long)T * Hkv * 2 * (D / 8) > 0x7fffffffLL)
+        (long long)n_pages * P > 0x7fffffffLL || !gain_ok(k_scale) || !gain_ok(v_scale))
         return DSPARK_ERR_INVALID_ARG;
     if (!cache || !slot || !k_out || !v_out || !aligned16(cache) || !aligned16(k_out) || !aligned16(v_out))
         return DSPARK_ERR_INVALID_ARG;

@@ -9,14 +9,15 @@
 //   scale = e4m3(max |y| over 16 dims / (6 g)), code = e2m1(y / (scale g)),
 //     both to nearest, ties to even (g = k_scale or v_scale).
 //
-// A CTA takes one token.  A row (head) belongs to D / 8 neighbouring lanes;
-// lane i holds two groups of four dims that rotate with each other: dims
-// 4i.. and rot/2 + 4i.. of the rotated part, or two groups of the rest.  So a
-// rotation needs no exchange, 16 dims of a scale are four neighbouring lanes,
-// and loads and stores stay contiguous.  The angles are reduced modulo 2 pi in
-// fp64 (a position of 2^20 times a frequency has 44 bits), then sine and
-// cosine run in fp32 once per token and frequency, shared by all heads.
-// Bytes bound it: each row is read and written once.
+// A CTA takes one token.  A row (head) belongs to D / 16 neighbouring lanes;
+// lane i holds two octets of dims that rotate with each other: dims 8i.. and
+// rot/2 + 8i.. of the rotated part, or two octets of the rest.  So a rotation
+// needs no exchange, the 16 dims of a scale are two neighbouring lanes, and
+// loads and stores are 16 bytes.  The angles are reduced to a turn in fp64 (a
+// position of 2^20 times a frequency has 44 bits), then sine and cosine run in
+// fp32 once per token and frequency, shared by all heads.
+// What bounds it is instruction issue, not bytes, hence two-lane fp32
+// arithmetic and several rows per thread.
 #include "cache.cuh"
 
 namespace dspark {
@@ -24,208 +25,271 @@ namespace dspark {
 namespace {
 
 constexpr int kMaxThreads = 512;
+constexpr int kManyTokens = 592;   // four CTAs on each of 148 SMs
 
-struct Quad {
-    float v[4];
+struct Oct {
+    float2 v[4];
 };
-__device__ __forceinline__ Quad load4(const float *p) {
-    const float4 x = __ldcs(reinterpret_cast<const float4 *>(p));
-    return {{x.x, x.y, x.z, x.w}};
+// Eight elements as loaded (widened when they are used, so that rows under
+// way take few registers).
+template <typename T> struct Raw;
+template <> struct Raw<float> { float4 a, b; };
+template <> struct Raw<__nv_bfloat16> { uint4 x; };
+__device__ __forceinline__ void load8(Raw<float> &r, const float *p) {
+    r.a = __ldcs(reinterpret_cast<const float4 *>(p));
+    r.b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
 }
-__device__ __forceinline__ Quad load4(const __nv_bfloat16 *p) {
-    const uint2 x = __ldcs(reinterpret_cast<const uint2 *>(p));
-    return {{bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y)}};
+__device__ __forceinline__ void load8(Raw<__nv_bfloat16> &r, const __nv_bfloat16 *p) {
+    r.x = __ldcs(reinterpret_cast<const uint4 *>(p));
 }
-__device__ __forceinline__ Quad weight4(const float *p) {
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
-    return {{x.x, x.y, x.z, x.w}};
+__device__ __forceinline__ Oct widen(const Raw<float> &r) {
+    return {{make_float2(r.a.x, r.a.y), make_float2(r.a.z, r.a.w), make_float2(r.b.x, r.b.y), make_float2(r.b.z, r.b.w)}};
 }
-__device__ __forceinline__ Quad weight4(const __nv_bfloat16 *p) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-    return {{bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y)}};
+__device__ __forceinline__ Oct widen(const Raw<__nv_bfloat16> &r) {
+    return {{make_float2(bf16lo(r.x.x), bf16hi(r.x.x)), make_float2(bf16lo(r.x.y), bf16hi(r.x.y)),
+             make_float2(bf16lo(r.x.z), bf16hi(r.x.z)), make_float2(bf16lo(r.x.w), bf16hi(r.x.w))}};
 }
-__device__ __forceinline__ void store4(float *p, const Quad &q) {
-    *reinterpret_cast<float4 *>(p) = make_float4(q.v[0], q.v[1], q.v[2], q.v[3]);
+__device__ __forceinline__ void store8(float *p, const Oct &q) {
+    *reinterpret_cast<float4 *>(p) = make_float4(q.v[0].x, q.v[0].y, q.v[1].x, q.v[1].y);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(q.v[2].x, q.v[2].y, q.v[3].x, q.v[3].y);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const Quad &q) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(q.v[0], q.v[1]), b = __floats2bfloat162_rn(q.v[2], q.v[3]);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-}
-
-// Four dims of a group of 16 (four neighbouring lanes) into the half record
-// at `half`: quad u of the token at page offset `off`.  NaN goes to 0 and
-// infinities to the largest value; both are reported.
-__device__ __forceinline__ bool quantise4(const Quad &q, float g, uint8_t *half, int u, int off, int P, int D,
-                                          bool live) {
-    bool bad = false;
-    float x[4], m = 0.f;
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Oct &q) {
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        bad |= !(fabsf(q.v[i]) <= 3.402823466e38f);
-        x[i] = q.v[i] == q.v[i] ? q.v[i] : 0.f;
-        m = fmaxf(m, fabsf(x[i]));
+        const __nv_bfloat162 x = __float22bfloat162_rn(q.v[i]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&x);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// x / y correctly rounded, from r = 1 / y correctly rounded: the remainder of
+// the first product is exact in an fma, and one step with it rounds the
+// quotient as a division would (P. Markstein, IBM J. Res. Dev. 34, 1990).
+// Finite operands, no overflow of x * r.
+__device__ __forceinline__ float quotient(float x, float y, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, y, x), r, q);
+}
+
+// Where a lane stores an octet of a row: offsets in a half record.
+struct Place {
+    int codes, scale;
+};
+
+// An octet of a group of 16 (this lane and its neighbour) to `half`.  NaN
+// goes to 0 and infinities to the largest value; both are reported.  g6 = 6 g,
+// r6 its reciprocal.  Values are clamped to where they saturate before they
+// are divided, so no quotient overflows.
+__device__ __forceinline__ bool quantise8(const Oct &q, float g, float g6, float r6, uint8_t *half, const Place &at,
+                                          bool lead, bool live) {
+    float x[8], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = i & 1 ? q.v[i / 2].y : q.v[i / 2].x;
+        m = fmaxf(m, fabsf(x[i]));           // passes NaN by
+    }
+    // A sum with 0 * x is 0 unless an x is infinite or NaN.
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd = fmaf(0.f, x[i], odd);
+    const bool bad = odd != 0.f;             // also for NaN
+    if (bad) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] : 0.f;
     }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     uint16_t s8;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fdiv_rn(m, 6.f * g)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(s8)
+        : "f"(0.f), "f"(quotient(fminf(m, 512.f * g6), g6, r6)));
     const float s = __half2float(__ushort_as_half((unsigned short)((s8 & 0x7f) << 7))) * 256.f * g;
     uint32_t codes = 0;
     if (s > 0.f) {
+        const float r = __frcp_rn(s), top = 8.f * s;
+        uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            uint32_t c;
+        for (int i = 0; i < 4; ++i) {
+            const float lo = quotient(fminf(fmaxf(x[2 * i], -top), top), s, r);
+            const float hi = quotient(fminf(fmaxf(x[2 * i + 1], -top), top), s, r);
             asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
-                : "=r"(c)
-                : "f"(__fdiv_rn(x[i], s)), "f"(__fdiv_rn(x[i + 1], s)));
-            codes |= c << (4 * i);
+                : "=r"(c[i])
+                : "f"(lo), "f"(hi));
         }
+        codes = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
     }
     if (live) {
-        *reinterpret_cast<uint16_t *>(half + (u / 8) * (P * 16) + off * 16 + (u % 8) * 2) = (uint16_t)codes;
-        if ((u & 3) == 0) half[half_scales_off(P, D) + off * (D / 16) + u / 4] = (uint8_t)(s8 & 0x7f);
+        *reinterpret_cast<uint32_t *>(half + at.codes) = codes;
+        if (lead) half[at.scale] = (uint8_t)(s8 & 0x7f);
     }
     return bad && live;
 }
 
 template <typename T, int D, bool WRITE>
-__global__ void __launch_bounds__(kMaxThreads) qk_norm_rope_kernel(const NormArgs a) {
-    constexpr int kLanes = D / 8;
-    __shared__ float2 cs[D / 2];
+__global__ void __launch_bounds__(kMaxThreads, 1) qk_norm_rope_kernel(const NormArgs a) {
+    constexpr int kLanes = D / 16;
+    constexpr int kUnder = sizeof(T) == 2 ? 3 : 2;     // rows under way per thread
+    __shared__ __align__(16) float2 cs[D / 2];
     const int t = blockIdx.x;
-    if (a.n_rows != nullptr && t >= __ldg(a.n_rows)) return;
     const int i = threadIdx.x % kLanes;
     const int rows = a.Hq + (WRITE ? 2 : 1) * a.Hkv;
-    const int n_rot = a.rot / 8;
+    const int n_rot = a.rot / 16;
     const bool rotated = i < n_rot;
-    // Quads of this lane, in units of four dims.
-    const int ua = rotated ? i : a.rot / 4 + (i - n_rot);
-    const int ub = rotated ? i + n_rot : a.rot / 4 + (D - a.rot) / 8 + (i - n_rot);
-    auto source = [&](int r) -> const T * {
-        if (r < a.Hq) return static_cast<const T *>(a.q) + (long long)t * a.q_stride + r * D;
-        if (r < a.Hq + a.Hkv) return static_cast<const T *>(a.k) + (long long)t * a.k_stride + (r - a.Hq) * D;
-        return static_cast<const T *>(a.v) + (long long)t * a.v_stride + (r - a.Hq - a.Hkv) * D;
+    // First dims of this lane's octets.
+    const int da = 8 * (rotated ? i : a.rot / 8 + (i - n_rot));
+    const int db = 8 * (rotated ? i + n_rot : a.rot / 8 + (D - a.rot) / 16 + (i - n_rot));
+    // Row r is at q_row + r * D, or the k_row or v_row that makes it so.
+    const T *q_row = static_cast<const T *>(a.q) + (long long)t * a.q_stride;
+    const T *k_row = static_cast<const T *>(a.k) + (long long)t * a.k_stride - a.Hq * D;
+    const T *v_row = WRITE ? static_cast<const T *>(a.v) + (long long)t * a.v_stride - (a.Hq + a.Hkv) * D : nullptr;
+    const int step = blockDim.x / kLanes, first = threadIdx.x / kLanes;
+    Raw<T> ra[kUnder], rb[kUnder];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < kUnder; ++u)
+            if (r0 + u * step < rows) {
+                const int r = r0 + u * step;
+                const T *p = (r < a.Hq ? q_row : r < a.Hq + a.Hkv ? k_row : v_row) + r * D;
+                load8(ra[u], p + da);
+                load8(rb[u], p + db);
+            }
     };
-    int r = threadIdx.x / kLanes;
-    const int step = blockDim.x / kLanes;
-    Quad xa, xb;
-    if (r < rows) {
-        const T *p = source(r);
-        xa = load4(p + 4 * ua);
-        xb = load4(p + 4 * ub);
+    // Everything the token needs is asked for before anything is waited for.
+    const int n_rows = a.n_rows != nullptr ? __ldg(a.n_rows) : a.T;
+    const int pos = a.rot > 0 ? __ldg(a.pos + t) : 0;
+    int slot = WRITE ? __ldg(a.slot + t) : -1;
+    if (t >= n_rows) return;
+    fetch(first);
+    // This lane's norm weights, as loaded.
+    Raw<T> wqa = {}, wqb = {}, wka = {}, wkb = {};
+    if (a.wq != nullptr) {
+        load8(wqa, static_cast<const T *>(a.wq) + da);
+        load8(wqb, static_cast<const T *>(a.wq) + db);
     }
-    if ((int)threadIdx.x < a.rot / 2) {
-        // t = pos * f exactly in fp64, less the nearest multiple of 2 pi.
-        const double x = (double)__ldg(a.pos + t) * (double)__ldg(a.inv_freq + threadIdx.x);
-        const double k = rint(x * 0.15915494309189533577);
-        const float y = (float)fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586232, x));
+    if (a.wk != nullptr) {
+        load8(wka, static_cast<const T *>(a.wk) + da);
+        load8(wkb, static_cast<const T *>(a.wk) + db);
+    }
+    for (int f = threadIdx.x; f < a.rot / 2; f += blockDim.x) {
+        // The angle in half turns, less whole turns, in fp64 (the product is exact).
+        const double x = (double)pos * (double)__ldg(a.inv_freq + f) * 0.15915494309189533577;
         float s, c;
-        sincosf(y, &s, &c);
-        cs[threadIdx.x] = make_float2(c, s);
+        sincospif((float)(2.0 * (x - rint(x))), &s, &c);
+        cs[f] = make_float2(c, s);
     }
-    int slot = -1, page = 0, off = 0;
+    uint8_t *record = nullptr;   // the token's page, head 0
+    Place pa = {}, pb = {};
+    const bool lead = (i & 1) == 0;
+    const int rec = record_bytes(a.P, D), kv_half = half_bytes(a.P, D);
     if (WRITE) {
-        slot = __ldg(a.slot + t);
         if (slot >= a.n_pages * a.P) {
             if (threadIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_PAGE_RANGE);
             slot = -1;
         }
-        if (slot >= 0) {
-            page = slot / a.P;
-            off = slot % a.P;
-        }
+        const int page = slot >= 0 ? slot / a.P : 0, off = slot >= 0 ? slot - page * a.P : 0;
+        record = a.cache + (size_t)page * a.Hkv * rec;
+        const int scales = half_scales_off(a.P, D) + off * (D / 16);
+        pa = {(da / 32 * a.P + off) * 16 + da % 32 / 2, scales + da / 16};
+        pb = {(db / 32 * a.P + off) * 16 + db % 32 / 2, scales + db / 16};
     }
     __syncthreads();
-    // Whole warps stay in the loop together (the shuffles name all lanes).
-    const int rounds = (rows + step - 1) / step;
+    // Whole warps stay in the loops together (the shuffles name all lanes).
     bool bad = false;
-    for (int k = 0; k < rounds; ++k, r += step) {
-        const bool live = r < rows;
-        Quad na, nb;
-        if (r + step < rows) {   // the next row is in flight while this one is worked on
-            const T *p = source(r + step);
-            na = load4(p + 4 * ua);
-            nb = load4(p + 4 * ub);
-        }
-        const bool is_v = r >= a.Hq + a.Hkv, is_k = !is_v && r >= a.Hq;
-        if (!live) {
+    const float rk = WRITE ? __frcp_rn(6.f * a.k_scale) : 0.f, rv = WRITE ? __frcp_rn(6.f * a.v_scale) : 0.f;
+    for (int r0 = first, k0 = 0; k0 < rows; r0 += kUnder * step, k0 += kUnder * step) {
+        if (k0 > 0) fetch(r0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) xa.v[e] = xb.v[e] = 0.f;
-        }
-        const void *w = is_k ? a.wk : a.wq;
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ss = fmaf(xa.v[e], xa.v[e], fmaf(xb.v[e], xb.v[e], ss));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (!is_v && w != nullptr) {
-            const float inv = __frsqrt_rn(ss * (1.f / D) + a.eps);
-            const Quad wa = weight4(static_cast<const T *>(w) + 4 * ua), wb = weight4(static_cast<const T *>(w) + 4 * ub);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                xa.v[e] = xa.v[e] * inv * wa.v[e];
-                xb.v[e] = xb.v[e] * inv * wb.v[e];
+        for (int u = 0; u < kUnder; ++u) {
+            if (k0 + u * step >= rows) break;          // the whole block
+            const int r = r0 + u * step;
+            const bool live = r < rows;
+            const bool is_v = r >= a.Hq + a.Hkv, is_k = !is_v && r >= a.Hq;
+            Oct xa = {}, xb = {};
+            if (live) {
+                xa = widen(ra[u]);
+                xb = widen(rb[u]);
             }
-        }
-        if (!is_v && rotated) {
-            if (a.interleaved) {
+            if (__any_sync(0xffffffffu, !is_v) && (a.wq != nullptr || a.wk != nullptr)) {
+                float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float2 ca = cs[2 * ua + e / 2], cb = cs[2 * ub + e / 2];
-                    const float a0 = xa.v[e], a1 = xa.v[e + 1], c0 = xb.v[e], c1 = xb.v[e + 1];
-                    xa.v[e] = a0 * ca.x - a1 * ca.y;
-                    xa.v[e + 1] = a1 * ca.x + a0 * ca.y;
-                    xb.v[e] = c0 * cb.x - c1 * cb.y;
-                    xb.v[e + 1] = c1 * cb.x + c0 * cb.y;
-                }
-            } else {
+                for (int e = 0; e < 4; ++e) s2 = fma2(xa.v[e], xa.v[e], fma2(xb.v[e], xb.v[e], s2));
+                float ss = s2.x + s2.y;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 c = cs[4 * ua + e];
-                    const float p = xa.v[e], q = xb.v[e];
-                    xa.v[e] = p * c.x - q * c.y;
-                    xb.v[e] = q * c.x + p * c.y;
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (!is_v && (is_k ? a.wk : a.wq) != nullptr) {
+                    const float inv = __frsqrt_rn(ss * (1.f / D) + a.eps);
+                    const float2 inv2 = make_float2(inv, inv);
+                    const Oct wa = widen(is_k ? wka : wqa), wb = widen(is_k ? wkb : wqb);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        xa.v[e] = mul2(mul2(xa.v[e], inv2), wa.v[e]);
+                        xb.v[e] = mul2(mul2(xb.v[e], inv2), wb.v[e]);
+                    }
                 }
             }
-        }
-        if (live && r < a.Hq) {
-            T *o = static_cast<T *>(a.q_out) + ((long long)t * a.Hq + r) * D;
-            store4(o + 4 * ua, xa);
-            store4(o + 4 * ub, xb);
-        }
-        if (live && is_k && a.k_out != nullptr) {
-            T *o = static_cast<T *>(a.k_out) + ((long long)t * a.Hkv + r - a.Hq) * D;
-            store4(o + 4 * ua, xa);
-            store4(o + 4 * ub, xb);
-        }
-        if (WRITE) {
-            // A warp whose rows are all queries has nothing to quantise.
-            if (__any_sync(0xffffffffu, live && r >= a.Hq)) {
-                const bool put = live && r >= a.Hq && slot >= 0;
-                const int h = is_v ? r - a.Hq - a.Hkv : (r >= a.Hq ? r - a.Hq : 0);
-                uint8_t *half = a.cache + ((size_t)page * a.Hkv + (put ? h : 0)) * record_bytes(a.P, D) +
-                                (is_v ? half_bytes(a.P, D) : 0);
-                const float g = is_v ? a.v_scale : a.k_scale;
-                bad |= quantise4(xa, g, half, ua, off, a.P, D, put);
-                bad |= quantise4(xb, g, half, ub, off, a.P, D, put);
+            if (!is_v && rotated) {
+                if (a.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 ca = cs[da / 2 + e], cb = cs[db / 2 + e];
+                        xa.v[e] = make_float2(xa.v[e].x * ca.x - xa.v[e].y * ca.y, xa.v[e].y * ca.x + xa.v[e].x * ca.y);
+                        xb.v[e] = make_float2(xb.v[e].x * cb.x - xb.v[e].y * cb.y, xb.v[e].y * cb.x + xb.v[e].x * cb.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(&cs[da + 2 * e]);   // two dims' (cos, sin)
+                        const float2 c = make_float2(c4.x, c4.z), s = make_float2(c4.y, c4.w);
+                        const float2 p = xa.v[e], q = xb.v[e];
+                        xa.v[e] = fma2(p, c, mul2(q, make_float2(-s.x, -s.y)));
+                        xb.v[e] = fma2(q, c, mul2(p, s));
+                    }
+                }
+            }
+            if (live && r < a.Hq) {
+                T *o = static_cast<T *>(a.q_out) + ((long long)t * a.Hq + r) * D;
+                store8(o + da, xa);
+                store8(o + db, xb);
+            }
+            if (live && is_k && a.k_out != nullptr) {
+                T *o = static_cast<T *>(a.k_out) + ((long long)t * a.Hkv + r - a.Hq) * D;
+                store8(o + da, xa);
+                store8(o + db, xb);
+            }
+            if (WRITE) {
+                // A warp whose rows are all queries has nothing to quantise.
+                if (__any_sync(0xffffffffu, live && r >= a.Hq)) {
+                    const bool put = live && r >= a.Hq && slot >= 0;
+                    const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
+                    uint8_t *half = record + (put ? h * rec + (is_v ? kv_half : 0) : 0);
+                    const float g = is_v ? a.v_scale : a.k_scale, g6 = 6.f * g, r6 = is_v ? rv : rk;
+                    bad |= quantise8(xa, g, g6, r6, half, pa, lead, put);
+                    bad |= quantise8(xb, g, g6, r6, half, pb, lead, put);
+                }
             }
         }
-        xa = na;
-        xb = nb;
     }
     if (WRITE && bad) flag_status(a.hdr, DSPARK_DEV_BAD_VALUE);
 }
 
 template <typename T, int D>
 cudaError_t launch_norm_d(const NormArgs &a, cudaStream_t st) {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 16;
     const bool write = a.cache != nullptr;
     const int rows = a.Hq + (write ? 2 : 1) * a.Hkv;
-    // As few rounds over the rows as 512 threads allow, the rows dealt evenly.
-    const int rounds = (rows * kLanes + kMaxThreads - 1) / kMaxThreads;
-    int threads = round_up((rows + rounds - 1) / rounds * kLanes, 32);
-    if (threads < D / 2) threads = D / 2;   // one thread per frequency
+    // Few tokens: all rows at once, for the latency.  Many: 128 threads with
+    // several rows each, so that what a thread sets up serves them all.
+    int threads = round_up(rows * kLanes, 32);
+    const int most = a.T >= kManyTokens ? 128 : kMaxThreads;
+    if (threads > most) threads = most;
     if (write)
         qk_norm_rope_kernel<T, D, true><<<a.T, threads, 0, st>>>(a);
     else
@@ -233,64 +297,47 @@ cudaError_t launch_norm_d(const NormArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&x);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Eight dims a thread: four bytes of codes and one scale.
+// A CTA per token, eight dims a thread and step: four bytes of codes and one scale.
+constexpr int kReadThreads = 128;
 template <typename T, int D>
-__global__ void __launch_bounds__(256) cache_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const ReadArgs a) {
     constexpr int kPer = D / 8;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int e = (int)(id % kPer);
-    const long long row = id / kPer;               // (token, K or V, head)
-    const int h = (int)(row % a.Hkv), part = (int)(row / a.Hkv % 2);
-    const long long t = row / (2 * a.Hkv);
-    if (t >= a.T) return;
-    const int slot = __ldg(a.slot + t);
+    const int t = blockIdx.x, slot = __ldg(a.slot + t);
     if (slot < 0) return;
     if (slot >= a.n_pages * a.P) {
-        if (e == 0 && h == 0 && part == 0) flag_status(a.hdr, DSPARK_DEV_PAGE_RANGE);
+        if (threadIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_PAGE_RANGE);
         return;
     }
-    const uint8_t *half = a.cache + ((size_t)(slot / a.P) * a.Hkv + h) * record_bytes(a.P, D) +
-                          part * half_bytes(a.P, D);
-    const int off = slot % a.P;
-    const uint32_t codes = *reinterpret_cast<const uint32_t *>(half + (e / 4) * (a.P * 16) + off * 16 + e % 4 * 4);
-    const uint32_t s = half[half_scales_off(a.P, D) + off * (D / 16) + e / 2];
-    uint32_t r[4];
-    e2m1x8_to_f16(codes, r[0], r[1], r[2], r[3]);
-    const uint32_t sf = scale_f16x2<0>(s);
-    const float g = part ? a.v_scale : a.k_scale;
-    float v[8];
+    const int page = slot / a.P, off = slot - page * a.P, rec = record_bytes(a.P, D), hb = half_bytes(a.P, D);
+    const uint8_t *record = a.cache + (size_t)page * a.Hkv * rec;
+    const int e = threadIdx.x % kPer;              // the same octet of every row
+    const int codes_at = (e / 4 * a.P + off) * 16 + e % 4 * 4, scale_at = half_scales_off(a.P, D) + off * (D / 16) + e / 2;
+    for (int row = threadIdx.x / kPer; row < 2 * a.Hkv; row += kReadThreads / kPer) {   // K heads, then V heads
+        const bool is_v = row >= a.Hkv;
+        const int h = is_v ? row - a.Hkv : row;
+        const uint8_t *half = record + h * rec + (is_v ? hb : 0);
+        const uint32_t codes = __ldg(reinterpret_cast<const uint32_t *>(half + codes_at));
+        const uint32_t s = __ldg(half + scale_at);
+        uint32_t r[4];
+        e2m1x8_to_f16(codes, r[0], r[1], r[2], r[3]);
+        const uint32_t sf = scale_f16x2<0>(s);
+        const float g = is_v ? a.v_scale : a.k_scale;
+        Oct v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t m = mul_f16x2(r[i], sf);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&m));
-        v[2 * i] = f.x * g;
-        v[2 * i + 1] = f.y * g;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t m = mul_f16x2(r[i], sf);
+            v.v[i] = mul2(__half22float2(*reinterpret_cast<const __half2 *>(&m)), make_float2(g, g));
+        }
+        store8(static_cast<T *>(is_v ? a.v_out : a.k_out) + ((size_t)t * a.Hkv + h) * D + e * 8, v);
     }
-    store8(static_cast<T *>(part ? a.v_out : a.k_out) + ((size_t)t * a.Hkv + h) * D + e * 8, v);
 }
 
 template <typename T>
 cudaError_t launch_read(const ReadArgs &a, cudaStream_t st) {
-    const long long n = (long long)a.T * a.Hkv * 2 * (a.D / 8);
-    const unsigned grid = (unsigned)((n + 255) / 256);
     if (a.D == 128)
-        cache_read_kernel<T, 128><<<grid, 256, 0, st>>>(a);
+        cache_read_kernel<T, 128><<<a.T, kReadThreads, 0, st>>>(a);
     else
-        cache_read_kernel<T, 64><<<grid, 256, 0, st>>>(a);
+        cache_read_kernel<T, 64><<<a.T, kReadThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
