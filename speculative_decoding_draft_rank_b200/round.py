@@ -25,9 +25,17 @@ def _dev(arr: np.ndarray, dtype: str, device) -> torch.Tensor:
 
 class DeviceRound:
     def __init__(self, inp: RoundInputs, knots_n, knots_t, budget: int, mode: int, device="cuda",
-                 tau=None, pinned_host: bool = False, Arec=None):
+                 tau=None, pinned_host: bool = False, Arec=None, cache=None, target=None):
         """Arec: the RNN head's recurrent matrix [r, r] (fp32 values, sent in
-        the round's dtype); None drafts with the Markov head."""
+        the round's dtype); None drafts with the Markov head.
+        cache: a kv_cache.PagedCache of this batch; the round then plans its
+        rows after scheduling and commits the emitted counts after
+        verification.  target(round, stream): enqueues the target pass between
+        the two (its logits go to t["Tlog"], rows 0..ell of each request);
+        None takes the logits as they are (run_from_host takes the host's)."""
+        if cache is not None and (cache.B != inp.B or cache.G < inp.G):
+            raise ValueError("the cache is for another batch or shorter blocks")
+        self.cache, self.target = cache, target
         self.inp = inp
         self.B, self.G, self.V, self.r, self.d = inp.B, inp.G, inp.V, inp.r, inp.d
         self.dt = inp.dtype
@@ -108,8 +116,13 @@ class DeviceRound:
             conf(main)
         _lib.dspark_schedule(o["S"], t["knots_n"], t["knots_t"], self.budget, self.mode, self.ws, o["ell"],
                              o["n_adm"], o["theta"], o["order"], main)
+        if self.cache is not None:
+            self.cache.plan(o["ell"], main)
         if verify:
+            if self.target is not None:
+                self.target(self, main)
             self.verify(main)
+            self.commit(main)
 
     # Inputs that change every round and feed drafting, confidence and the
     # draws; the target logits follow once the admitted lengths are known.
@@ -134,6 +147,7 @@ class DeviceRound:
             self.run(main, overlap_confidence, verify=False)
             _lib.dspark_gather_admitted_targets(self.host["Tlog"], self.t["Tlog"], self.o["ell"], main)
             self.verify(main)
+            self.commit(main)
         self.download(main)
 
     def host_round_bytes(self):
@@ -166,6 +180,11 @@ class DeviceRound:
             _lib.dspark_verify(t["Tlog"], t["L"], t["U"], t["Wt"], t["x0"], o["x"], o["pd_x"], o["rowmax"],
                                o["rowsum"], t["temp"], t["u_accept"], t["u_final"], o["ell"], self.ws, o["acc"],
                                o["tokens"], o["nout"], o["pt_x"], stream)
+
+    def commit(self, stream=None):
+        """Keep the emitted tokens' keys and values in the cache, if there is one."""
+        if self.cache is not None:
+            self.cache.commit(self.o["nout"], None, stream)
 
     def upload(self, stream=None):
         """Copy every input from pinned host memory (end-to-end timing)."""

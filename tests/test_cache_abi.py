@@ -1,0 +1,130 @@
+"""The cache and attention calls without a GPU: every documented refusal
+comes back from the host checks, before any CUDA call."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from speculative_decoding_draft_rank_b200 import _lib, build
+
+A = ctypes.c_void_p(0x100000)
+ODD = ctypes.c_void_p(0x100008)
+WS = ctypes.c_void_p(0x200000)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def test_sizes(lib):
+    assert _lib.dspark_cache_record_bytes(64, 128) == 9216 and _lib.dspark_cache_record_bytes(16, 64) == 1152
+    assert _lib.dspark_cache_record_bytes(48, 128) == 0 and _lib.dspark_cache_record_bytes(64, 96) == 0
+    f = _lib.dspark_cache_attention_workspace_size
+    assert 0 < f(1, 1, 1, 64) < f(4096, 64, 8, 128) < 16 << 20
+    assert f(0, 8, 8, 64) == 0 and f(4097, 8, 8, 64) == 0 and f(1, 7, 2, 64) == 0 and f(1, 8, 8, 80) == 0
+    assert f(1, 2048, 8, 64) == 0
+
+
+def _plan(lib, B=4, G=5, P=64, mp=8, n=100, ws=WS, wsb=256, null=None):
+    p = [A] * 10
+    if null is not None:
+        p[null] = None
+    return lib.dspark_cache_plan(p[0], p[1], B, G, P, mp, n, p[2], p[3], p[4], p[5], ws, wsb, p[6], p[7], p[8], p[9],
+                                 None)
+
+
+def test_plan_refusals(lib):
+    for bad in (dict(B=0), dict(B=4097), dict(G=-1), dict(G=(1 << 20) + 1), dict(B=4096, G=4096), dict(P=48),
+                dict(mp=0), dict(n=0), dict(n=1 << 26), dict(mp=1 << 25)):
+        assert _plan(lib, **bad) == 1, bad
+    for k in range(10):
+        assert _plan(lib, null=k) == 1, k
+    assert _plan(lib, ws=None) == 3 and _plan(lib, wsb=255) == 3 and _plan(lib, ws=ctypes.c_void_p(0x200010)) == 3
+
+
+def test_commit_refusals(lib):
+    f = lib.dspark_cache_commit
+
+    def call(B=4, P=64, mp=8, n=100, ws=WS, wsb=256, null=None):
+        p = [A] * 8
+        if null is not None:
+            p[null] = None
+        return f(p[0], p[1], p[2], None, B, P, mp, n, p[3], p[4], p[5], p[6], ws, wsb, p[7], None)
+
+    assert call(B=0) == 1 and call(P=8) == 1 and call(mp=0) == 1 and call(n=0) == 1
+    for k in range(8):
+        assert call(null=k) == 1, k
+    assert call(ws=None) == 3 and call(wsb=0) == 3
+
+
+def _norm(lib, q=A, qs=1024, k=A, ks=512, v=A, vs=512, wq=A, wk=A, eps=1e-6, pos=A, freq=A, rot=64, T=4, Hq=8, Hkv=4,
+          D=128, dt=1, qo=A, ko=A, cache=A, slot=A, P=64, n=10, kg=1.0, vg=1.0, ws=WS, wsb=256):
+    return lib.dspark_qk_norm_rope(q, qs, k, ks, v, vs, wq, wk, eps, pos, freq, rot, 0, None, T, Hq, Hkv, D, dt, qo,
+                                   ko, cache, slot, P, n, kg, vg, ws, wsb, None)
+
+
+def test_norm_refusals(lib):
+    assert _norm(lib, dt=7) == 2
+    for bad in (dict(T=-1), dict(T=(1 << 24) + 1), dict(Hq=6), dict(Hkv=0), dict(Hq=2048, Hkv=1024), dict(D=96),
+                dict(rot=48), dict(rot=160), dict(rot=-32), dict(eps=-1.0), dict(eps=math.nan), dict(q=None),
+                dict(k=None), dict(qo=None), dict(ko=None, cache=None), dict(pos=None), dict(freq=None),
+                dict(v=None), dict(slot=None), dict(P=24), dict(n=0), dict(kg=0.0), dict(vg=-1.0),
+                dict(kg=math.inf), dict(vg=math.nan), dict(q=ODD), dict(k=ODD), dict(v=ODD), dict(wq=ODD),
+                dict(wk=ODD), dict(qo=ODD), dict(ko=ODD), dict(cache=ODD), dict(qs=1023), dict(qs=1028),
+                dict(ks=511), dict(vs=500)):
+        assert _norm(lib, **bad) == 1, bad
+    assert _norm(lib, ws=None) == 3 and _norm(lib, wsb=128) == 3
+    assert _norm(lib, T=0) == 0                     # nothing to do, nothing launched
+
+
+def test_read_refusals(lib):
+    def call(cache=A, slot=A, T=3, Hkv=4, D=64, P=16, n=9, kg=1.0, vg=1.0, dt=1, ko=A, vo=A, ws=WS, wsb=256):
+        return lib.dspark_cache_read(cache, slot, T, Hkv, D, P, n, kg, vg, dt, ko, vo, ws, wsb, None)
+
+    assert call(dt=3) == 2
+    for bad in (dict(cache=None), dict(slot=None), dict(T=-1), dict(Hkv=0), dict(D=32), dict(P=0), dict(n=0),
+                dict(kg=0.0), dict(vg=math.inf), dict(ko=None), dict(vo=ODD), dict(cache=ODD)):
+        assert call(**bad) == 1, bad
+    assert call(ws=None) == 3 and call(T=0) == 0
+
+
+def _attend(lib, q=A, qs=1024, cache=A, table=A, start=A, kv=A, B=4, T=24, Hq=8, Hkv=4, D=128, P=64, mp=8, n=100,
+            scale=0.1, kg=1.0, vg=1.0, window=0, dt=1, ws=WS, wsb=1 << 24, out=A):
+    return lib.dspark_cache_attention(q, qs, cache, table, start, kv, B, T, Hq, Hkv, D, P, mp, n, scale, kg, vg,
+                                      window, dt, ws, wsb, out, None)
+
+
+def test_attention_refusals(lib):
+    assert _attend(lib, dt=0) == 2 and _attend(lib, dt=5) == 2
+    for bad in (dict(B=0), dict(B=5000), dict(T=-1), dict(Hq=9), dict(Hkv=0), dict(D=256), dict(P=100), dict(mp=0),
+                dict(n=0), dict(scale=math.nan), dict(scale=math.inf), dict(kg=0.0), dict(vg=-2.0), dict(window=-1),
+                dict(q=None), dict(cache=None), dict(table=None), dict(start=None), dict(kv=None), dict(out=None),
+                dict(q=ODD), dict(cache=ODD), dict(qs=1000), dict(qs=1028),
+                dict(B=4096, T=1 << 20, Hq=64, Hkv=64, mp=1 << 20, P=128, n=1 << 20)):
+        assert _attend(lib, **bad) == 1, bad
+    assert _attend(lib, ws=None) == 3 and _attend(lib, wsb=4096) == 3
+    assert _attend(lib, T=0) == 0
+
+
+def test_injected_errors_come_back(lib, monkeypatch):
+    monkeypatch.setenv("DSPARK_INJECT_ERROR", "dspark_cache_attention=4")
+    assert _attend(lib) == 4
+    monkeypatch.setenv("DSPARK_INJECT_ERROR", "dspark_cache_plan=4")
+    assert _plan(lib) == 4
+
+
+def test_binding_refuses_host_tensors_and_wrong_types(lib):
+    i = torch.zeros(8, dtype=torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        _lib.dspark_cache_plan(i[:2], i[:2], 1, torch.zeros(2, 4, dtype=torch.int32), i[:2], i, i[:1], 16, ws, i[:3],
+                               i[:2], i[:4], i[:4])
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        _lib.dspark_qk_norm_rope(q, q, None, None, 1e-6, None, None, False, None, q, q, ws)
+    with pytest.raises(ValueError):
+        _lib.dspark_cache_attention(q, torch.zeros(4, 2, 99, dtype=torch.uint8), torch.zeros(1, 4, dtype=torch.int32),
+                                    i[:2], i[:1], 16, 0.1, 0, ws, q)
