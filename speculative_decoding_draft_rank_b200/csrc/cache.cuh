@@ -137,10 +137,11 @@ struct AttnArgs {
     long long budget;
 };
 size_t attention_ws_bytes(int D);
-// Tiles of 128 keys a call can need at most; the kernel counts them in 32 bits.
+// Tiles of 128 keys a call can need at most; the kernel adds up their costs
+// (at most 16 a tile and 70 an item) in 32 bits.
 inline bool attention_tiles_fit(int B, int T, int Hkv, int group, int P, int max_pages) {
     const double items = (double)Hkv * ((double)B + (double)T * group / 48.0 + 1.0);
-    return items * ((double)max_pages * P / 128.0 + 2.0) < 2.0e9;
+    return items * (16.0 * ((double)max_pages * P / 128.0 + 2.0) + 70.0) < 2.0e9;
 }
 cudaError_t launch_cache_attention(AttnArgs a, void *ws, cudaStream_t st);
 

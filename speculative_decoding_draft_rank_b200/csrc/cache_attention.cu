@@ -62,7 +62,7 @@ constexpr int kThreads = (kWarpLoad + 4) * 32;
 constexpr int kMaxCtas = 160;
 constexpr long long kWaitBudget = 4000000000LL;
 constexpr float kRaise = 8.f;     // log2 room above the running maximum
-constexpr int kDescInts = 8;      // rem, q0, r0, nr, h, quota
+constexpr int kDescInts = 8;      // CTAs that go on with the item, q0, r0, nr, h
 
 // TMEM columns.
 constexpr int kColK = 0, kColS = 192, kColO = 384, kColL = 432, kColOne = 480;
@@ -86,7 +86,8 @@ struct Rows {
     float4 mul_m[kRows / 2];
     int2 lim[kRows];         // visible keys [x, y)
     int orow[kRows];         // output row (token * Hq + head)
-    int nr, base, t0, t1, nt, q0, r0, h;   // the piece: rows, first key, its tiles of the item's nt, where it belongs
+    int nr, base, t0, t1, nt, q0, r0, h, last;   // the piece: rows, first key, its tiles of the item's nt, where it
+                                                // belongs; the CTA of the item's last tile
     int version;             // times the maxima were raised
     __device__ __forceinline__ float &mul(int r) { return reinterpret_cast<float *>(&mul_m[r / 2])[r & 1]; }
     __device__ __forceinline__ float &neg_max(int r) { return reinterpret_cast<float *>(&mul_m[r / 2])[2 + (r & 1)]; }
@@ -104,7 +105,7 @@ struct Misc {
     uint64_t q_full[2], q_empty[2], m_full[2], drain[2];   // m_full: the piece's first maxima are set
     uint32_t tmem;
     int abort;
-    int scan[16];
+    int2 scan[16];
 };
 
 struct Req {
@@ -139,35 +140,57 @@ __device__ __forceinline__ Block row_block(const AttnArgs &a, const Req &q, int 
     return k;
 }
 
+// What a tile costs, and what changing to another item does (its last
+// products and result; the first maxima), in units of about 125 cycles:
+// measured 1600 cycles a tile up to 32 rows, 2000 for 48 rows, 9000 an item
+// in a run of some 20 tiles each.  CTAs get equal costs rather than equal tiles.
+__device__ __forceinline__ int tile_cost(const Block &k) { return k.nr <= 32 ? 13 : 16; }
+constexpr int kItemCost = 70, kMinQuota = 16;   // a quota holds the start of at least one tile
+__device__ __forceinline__ int item_cost(const Block &k) { return k.nt * tile_cost(k) + kItemCost; }
+
+// The item in which position `pos` of the batch's costs lies, its first tile
+// that starts there or later (nt: none), and the tiles of the batch before that.
+struct Spot {
+    int b, rb, h, t, start, tiles;   // start: position of the item
+    Req q;
+    Block k;
+};
+__device__ __forceinline__ Spot spot_at(const AttnArgs &a, const int *cost, const int *tiles, int pos) {
+    Spot p;
+    int lo = 0, hi = a.B;                // the request: cost[b] <= pos < cost[b + 1]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cost[mid] <= pos) lo = mid; else hi = mid;
+    }
+    p.b = lo;
+    p.q = load_req(a, lo);
+    int off = pos - cost[lo], c = 0;
+    p.tiles = tiles[lo];
+    for (p.rb = 0;; ++p.rb) {
+        p.k = row_block(a, p.q, p.rb);
+        c = item_cost(p.k);
+        if (off < c * a.Hkv) break;
+        off -= c * a.Hkv;
+        p.tiles += p.k.nt * a.Hkv;
+    }
+    p.h = off / c;
+    off -= p.h * c;
+    p.start = pos - off;
+    const int w = tile_cost(p.k);
+    p.t = min(p.k.nt, (off + w - 1) / w);
+    p.tiles += p.h * p.k.nt + p.t;
+    return p;
+}
+
 // This CTA's run of tiles, piece by piece (a piece: consecutive tiles of one item).
 struct Walk {
     const AttnArgs &a;
     int left;                // tiles left in the run
-    int b, rb, h, t0, t1;
+    int b, rb, h, t0, t1, start;
     Req q;
     Block k;
-    __device__ __forceinline__ Walk(const AttnArgs &args, const int *prefix, int w0, int w1) : a(args) {
-        left = w1 - w0;
-        int lo = 0, hi = a.B;                // the request holding tile w0: prefix[b] <= w0 < prefix[b + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= w0) lo = mid; else hi = mid;
-        }
-        b = lo;
-        q = load_req(a, b);
-        int off = w0 - prefix[b];
-        for (rb = 0;; ++rb) {
-            k = row_block(a, q, rb);
-            if (off < k.nt * a.Hkv) break;
-            off -= k.nt * a.Hkv;
-        }
-        h = off / k.nt;
-        t0 = off - h * k.nt;
-        t1 = min(k.nt, t0 + left);
-    }
-    __device__ __forceinline__ bool next() {   // false: the run is done
-        left -= t1 - t0;
-        if (left <= 0) return false;
+    __device__ __forceinline__ void next_item() {
+        start += item_cost(k);
         if (++h == a.Hkv) {
             h = 0;
             if (rb + 1 < row_blocks(a, q)) {
@@ -179,6 +202,22 @@ struct Walk {
             k = row_block(a, q, rb);
         }
         t0 = 0;
+    }
+    __device__ __forceinline__ Walk(const AttnArgs &args, const Spot &p, int tiles) : a(args), left(tiles) {
+        b = p.b;
+        rb = p.rb;
+        h = p.h;
+        t0 = p.t;
+        start = p.start;
+        q = p.q;
+        k = p.k;
+        if (t0 == k.nt) next_item();
+        t1 = min(k.nt, t0 + left);
+    }
+    __device__ __forceinline__ bool next() {   // false: the run is done
+        left -= t1 - t0;
+        if (left <= 0) return false;
+        next_item();
         t1 = min(k.nt, left);
         return true;
     }
@@ -380,32 +419,37 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);   // still known to be shared memory
     Misc &ms = *reinterpret_cast<Misc *>(sm + Y::misc);
-    // In the probabilities' place: the walks that read it are set up before the
-    // first scores, and so before the first probabilities.
-    int *prefix = reinterpret_cast<int *>(sm + Y::p);
+    // In the probabilities' place: read for the last time before the roles begin.
+    int *prefix = reinterpret_cast<int *>(sm + Y::p), *before_t = prefix + 4096;   // costs and tiles before a request
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // Tiles of every request, and their prefix: thread t sums a run of requests.
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int sum = 0;
+    int sum = 0, sum_t = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
         const Req q = load_req(a, b);
         bad |= __ldg(a.kv_len + b) != q.L || __ldg(a.q_start + b) != q.q0 || __ldg(a.q_start + b + 1) != q.q0 + q.n;
-        int t = 0;
-        for (int rb = 0; rb < row_blocks(a, q); ++rb) t += row_block(a, q, rb).nt;
         prefix[b] = sum;
-        sum += t * a.Hkv;
+        before_t[b] = sum_t;
+        for (int rb = 0; rb < row_blocks(a, q); ++rb) {
+            const Block k = row_block(a, q, rb);
+            sum += item_cost(k) * a.Hkv;
+            sum_t += k.nt * a.Hkv;
+        }
     }
     if (bad && blockIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_LENGTH_RANGE);
-    int inc = sum;
+    int inc = sum, inc_t = sum_t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const int y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_t, o);
+        if (lane >= o) {
+            inc += y;
+            inc_t += z;
+        }
     }
-    if (lane == 31) ms.scan[warp] = inc;
+    if (lane == 31) ms.scan[warp] = make_int2(inc, inc_t);
     if (tid == 0) {
         ms.abort = 0;
         for (int i = 0; i < kAhead; ++i) {
@@ -430,15 +474,30 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         fence_barrier_init();
     }
     __syncthreads();
-    int before = inc - sum, total = 0;
+    int before = inc - sum, total = 0, before_tiles = inc_t - sum_t, all_tiles = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += ms.scan[w];
-        total += ms.scan[w];
+        const int2 x = ms.scan[w];
+        if (w < warp) {
+            before += x.x;
+            before_tiles += x.y;
+        }
+        total += x.x;
+        all_tiles += x.y;
     }
-    for (int b = b0; b < b1; ++b) prefix[b] += before;
-    const int quota = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int w0 = min(total, (int)blockIdx.x * quota), w1 = min(total, w0 + quota);
-    if (w0 >= w1) {   // the whole CTA: no work, nothing left unfinished
+    for (int b = b0; b < b1; ++b) {
+        prefix[b] += before;
+        before_t[b] += before_tiles;
+    }
+    __syncthreads();
+    const int quota = max(kMinQuota, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    const long long w0 = (long long)blockIdx.x * quota, w1 = w0 + quota;
+    Spot spot = {};
+    int tiles = 0;
+    if (w0 < total) {
+        spot = spot_at(a, prefix, before_t, (int)w0);
+        tiles = (w1 < total ? spot_at(a, prefix, before_t, (int)w1).tiles : all_tiles) - spot.tiles;
+    }
+    if (tiles <= 0) {   // the whole CTA: no work, nothing left unfinished
         if (tid == 0) a.desc[blockIdx.x * kDescInts] = 0;
         return;
     }
@@ -452,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     tc_fence_after();
     const uint32_t tm = ms.tmem;
     volatile int *abort = &ms.abort;
-    const int tiles = w1 - w0;
     int g = 0;   // tiles done by this role
 
     if (warp < 4 * kGroups) {
@@ -696,31 +754,46 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     tc_fence_after();
                     const bool whole = t0 == 0 && t1 == rw.nt;
                     const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-#pragma unroll 1
-                    for (int r0 = 0; r0 < nr; r0 += 16) {
+                    // O is read and its place given back before the results are stored.
+                    uint32_t y[kRows / 2];
+#pragma unroll
+                    for (int c = 0; c < kRows / 16; ++c) {
+                        if (c * 16 >= nr) break;
                         __syncwarp();
                         uint32_t o[16], l[16];
-                        tmem_ld16(tm + lane_base + kColO + r0, o);
-                        tmem_ld16(tm + lane_base + kColL + r0, l);
+                        tmem_ld16(tm + lane_base + kColO + c * 16, o);
+                        tmem_ld16(tm + lane_base + kColL + c * 16, l);
                         tmem_ld_wait();
                         if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
+                            for (int i = 0; i < 16; i += 2) {
                                 // No visible key: the sum is 0 and so is O.
-                                const float ll = __uint_as_float(l[i]), inv = ll == 0.f ? 0.f : rcp(ll) * a.v_mul;
-                                const float y = __uint_as_float(o[i]) * inv;
-                                if (r0 + i < nr && key < D)
-                                    a.out[(long long)rw.orow[r0 + i] * D + key] = __float2bfloat16_rn(y);
+                                const float l0 = __uint_as_float(l[i]), l1 = __uint_as_float(l[i + 1]);
+                                const float v0 = l0 == 0.f ? 0.f : rcp(l0) * a.v_mul, v1 = l1 == 0.f ? 0.f : rcp(l1) * a.v_mul;
+                                const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(o[i]) * v0,
+                                                                               __uint_as_float(o[i + 1]) * v1);
+                                y[c * 8 + i / 2] = *reinterpret_cast<const uint32_t *>(&z);
                             }
                         } else {
-                            float *po = a.part_o + ((size_t)slot * kRows + r0) * D + key;
+                            float *po = a.part_o + ((size_t)slot * kRows + c * 16) * D + key;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                if (r0 + i < nr && key < D) po[i * D] = __uint_as_float(o[i]);
-                                if (r0 + i < nr && key == i)
-                                    a.part_ml[slot * kRows + r0 + i] =
-                                        make_float2(-rw.neg_max(r0 + i), __uint_as_float(l[i]));
+                                const int r = c * 16 + i;
+                                if (r < nr && key < D) po[i * D] = __uint_as_float(o[i]);
+                                if (r < nr && key == i)
+                                    a.part_ml[slot * kRows + r] = make_float2(-rw.neg_max(r), __uint_as_float(l[i]));
                             }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.turn[sg]);
+                    if (whole && key < D) {
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r) {
+                            if (r >= nr) break;
+                            const uint16_t v = (uint16_t)(r & 1 ? y[r / 2] >> 16 : y[r / 2]);
+                            reinterpret_cast<uint16_t *>(a.out)[(long long)rw.orow[r] * D + key] = v;
                         }
                     }
                     if (!whole && t0 == 0 && key == 0) {
@@ -729,13 +802,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                         d[2] = rw.r0;
                         d[3] = nr;
                         d[4] = rw.h;
-                        d[5] = quota;
-                        d[0] = rw.nt - t1;
+                        d[0] = rw.last - (int)blockIdx.x;   // CTAs that go on with it
                     }
-                    tc_fence_before();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.turn[sg]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.turn[sg]);
                 ph ^= 1;
             }
             __syncwarp();
@@ -747,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         // before they are used.
         const int ppt = kTile / a.P;
         const unsigned long long rec_bytes = record_bytes(a.P, D);
-        Walk wk(a, prefix, w0, w1);
+        Walk wk(a, spot, tiles);
         for (int t = wk.t0; g < tiles; ++g) {
             const int key0 = wk.k.base + t * kTile, np = min(ppt, max(0, (wk.k.hi - key0 + a.P - 1) / a.P));
             unsigned long long rec = 0;
@@ -830,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         constexpr int kLanes = D / 16, kPass = 32 / kLanes, kBatch = 2;
         const int part = lane % kLanes, rsub = lane / kLanes;
         int piece = 0;
-        Walk wk(a, prefix, w0, w1);
+        Walk wk(a, spot, tiles);
         do {
             Rows &rw = ms.rows[piece & 1];
             uint8_t *qs = sm + Y::q + (piece & 1) * Y::kQBytes;
@@ -856,6 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                 rw.q0 = wk.q.q0;
                 rw.r0 = wk.k.r0;
                 rw.h = wk.h;
+                rw.last = (wk.start + (wk.k.nt - 1) * tile_cost(wk.k)) / quota;
                 rw.version = 0;
             }
 #pragma unroll 1
@@ -937,11 +1010,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
 template <int D>
 __global__ void __launch_bounds__(256) cache_attention_join(const AttnArgs a) {
     const int32_t *d = a.desc + blockIdx.x * kDescInts;
-    const int rem = d[0];
-    if (rem <= 0) return;
+    const int more = d[0];
+    if (more <= 0) return;
     const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (r >= d[3]) return;
-    const int parts = 1 + (rem + d[5] - 1) / d[5];
+    const int parts = 1 + more;
     // Part 0 is this CTA's second slot, part i > 0 the first slot of CTA blockIdx.x + i.
     auto slot = [&](int i) { return i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i); };
     float m = -INFINITY;
@@ -974,7 +1047,7 @@ template <int D>
 cudaError_t launch_d(const AttnArgs &a, int grid, cudaStream_t st) {
     const size_t bytes = Lay<D>::misc + sizeof(Misc) + 1024;
     static_assert(Lay<D>::misc + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory of an SM");
-    static_assert(4096 * sizeof(int) <= kRing * Lay<D>::kPBytes, "the prefix of the largest batch");
+    static_assert(2 * 4096 * sizeof(int) <= kRing * Lay<D>::kPBytes, "the prefix of the largest batch");
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(cache_attention_kernel<D>), bytes, done);
     if (e != cudaSuccess) return e;
