@@ -417,7 +417,8 @@ size_t dspark_cache_record_bytes(int P, int D);
  * Inputs:  ctx [B], ell [B] (clamped to [0, G], DSPARK_DEV_ELL_RANGE).
  * Outputs: q_start_out [B+1]; kv_len_out [B] = ctx + n_b (0 for an empty
  *          seat); slot_out and pos_out [B * (G+1)], -1 behind the last row.
- * Limits:  B <= 4096, 0 <= G <= 2^20, B * (G+1) <= 2^24, n_pages * P < 2^31.
+ * Limits:  B <= 4096, 0 <= G <= 2^20, B * (G+1) <= 2^24, n_pages * P < 2^31,
+ *          max_pages * P <= 2^30.
  * Calling it again for the same lengths gives the same outputs and takes no
  * further pages.  One launch. */
 dspark_status dspark_cache_plan(const int32_t *ctx, const int32_t *ell, int B, int G, int P, int max_pages,
@@ -476,7 +477,8 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
  * Inputs:  q [T, Hq, D] bf16, tokens q_stride elements apart as above; table
  *          [B, max_pages], q_start [B+1], kv_len [B] as dspark_cache_plan
  *          leaves them, after the round's keys were written.
- * Outputs: out [T, Hq, D] bf16, dense.
+ * Outputs: out [T, Hq, D] bf16, dense, not overlapping q
+ *          (DSPARK_ERR_INVALID_ARG).
  * fp32 scores, maxima and sums; probabilities enter the second product in
  * f16, keys, values and queries exactly.  Any n_b and any group Hq / Hkv.
  * Deterministic.  Two launches.  bf16 only (DSPARK_ERR_UNSUPPORTED_DTYPE). */

@@ -13,7 +13,7 @@ dspark_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK :
 
 bool table_ok(int B, int P, int max_pages, int n_pages) {
     return B >= 1 && B <= 4096 && page_ok(P) && max_pages >= 1 && n_pages >= 1 &&
-           (long long)n_pages * P <= 0x7fffffffLL && (long long)max_pages * P <= 0x7fffffffLL - P;
+           (long long)n_pages * P <= 0x7fffffffLL && (long long)max_pages * P <= (1LL << 30);
 }
 bool heads_ok(int Hq, int Hkv) { return Hkv >= 1 && Hq >= Hkv && Hq <= 1024 && Hq % Hkv == 0; }
 bool gain_ok(float g) { return g > 0.f && std::isfinite(g); }
@@ -128,6 +128,10 @@ dspark_status dspark_cache_attention(const void *q, long long q_stride, const vo
         return DSPARK_ERR_INVALID_ARG;
     if (dspark_status s = check_ws(ws, ws_bytes, attention_ws_bytes(D))) return s;
     if (T == 0) return DSPARK_OK;
+    // Parts of an item read its queries while another part's results are out.
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t q1 = q0 + ((size_t)(T - 1) * (size_t)q_stride + (size_t)Hq * D) * 2, o1 = o0 + (size_t)T * Hq * D * 2;
+    if (q0 < o1 && o0 < q1) return DSPARK_ERR_INVALID_ARG;
     AttnArgs a{};
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.q_stride = q_stride;

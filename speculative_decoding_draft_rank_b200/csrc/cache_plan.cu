@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const Comm
         }
         int out = -1;
         if (c >= 0 && (a.done == nullptr || __ldg(a.done + b) == 0)) {
-            const int n = max(0, __ldg(a.q_start + b + 1) - __ldg(a.q_start + b));
+            const int s0 = max(0, __ldg(a.q_start + b)), s1 = max(s0, __ldg(a.q_start + b + 1));
+            const int n = min(s1 - s0, a.max_pages * a.P);
             const int k = __ldg(a.nout + b);
             if (k < 0 || k > n) flags |= DSPARK_DEV_LENGTH_RANGE;
             out = min(c, a.max_pages * a.P) + min(max(k, 0), n);

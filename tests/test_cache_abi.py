@@ -38,7 +38,7 @@ def _plan(lib, B=4, G=5, P=64, mp=8, n=100, ws=WS, wsb=256, null=None):
 
 def test_plan_refusals(lib):
     for bad in (dict(B=0), dict(B=4097), dict(G=-1), dict(G=(1 << 20) + 1), dict(B=4096, G=4096), dict(P=48),
-                dict(mp=0), dict(n=0), dict(n=1 << 26), dict(mp=1 << 25)):
+                dict(mp=0), dict(n=0), dict(n=1 << 26), dict(mp=(1 << 24) + 1)):
         assert _plan(lib, **bad) == 1, bad
     for k in range(10):
         assert _plan(lib, null=k) == 1, k
@@ -92,7 +92,7 @@ def test_read_refusals(lib):
 
 
 def _attend(lib, q=A, qs=1024, cache=A, table=A, start=A, kv=A, B=4, T=24, Hq=8, Hkv=4, D=128, P=64, mp=8, n=100,
-            scale=0.1, kg=1.0, vg=1.0, window=0, dt=1, ws=WS, wsb=1 << 24, out=A):
+            scale=0.1, kg=1.0, vg=1.0, window=0, dt=1, ws=WS, wsb=1 << 24, out=ctypes.c_void_p(0x900000)):
     return lib.dspark_cache_attention(q, qs, cache, table, start, kv, B, T, Hq, Hkv, D, P, mp, n, scale, kg, vg,
                                       window, dt, ws, wsb, out, None)
 
@@ -106,6 +106,8 @@ def test_attention_refusals(lib):
                 dict(B=4096, T=1 << 20, Hq=64, Hkv=64, mp=1 << 20, P=128, n=1 << 20)):
         assert _attend(lib, **bad) == 1, bad
     assert _attend(lib, ws=None) == 3 and _attend(lib, wsb=4096) == 3
+    for at in (0x100000, 0x100000 + 24 * 2048 - 16, 0x100000 - 24 * 2048 + 16):   # out over q
+        assert _attend(lib, out=ctypes.c_void_p(at)) == 1
     assert _attend(lib, T=0) == 0
 
 

@@ -297,6 +297,61 @@ def test_attention_many_requests():
     _check_attention(q, cache, table, n, kv.astype(np.int32), 16, 0.125)
 
 
+@pytest.mark.parametrize("seed,B,Hq,Hkv,D,P,top,most,window", [
+    (0, 40, 8, 2, 128, 64, 2500, 6, 0), (1, 150, 6, 3, 64, 16, 700, 17, 100), (2, 3, 48, 2, 64, 128, 9000, 4, 0),
+    (3, 301, 4, 4, 64, 32, 260, 3, 0), (4, 17, 64, 1, 128, 32, 1500, 9, 513)])
+def test_attention_ragged_batches(seed, B, Hq, Hkv, D, P, top, most, window):
+    """Batches whose items are cut over the machine, every row against fp64 (torch, one request at a time)."""
+    rng = np.random.default_rng(seed)
+    n = rng.integers(0, most + 1, B)
+    kv = n + (rng.random(B) ** 2 * top).astype(np.int64)
+    mp = int(-(-kv.max() // P)) + 1
+    n_pages = B * mp
+    table = torch.from_numpy(rng.permutation(n_pages).reshape(B, mp).astype(np.int32)).cuda()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cache = torch.randint(0, 256, (n_pages, Hkv, _lib.dspark_cache_record_bytes(P, D)), generator=g, device="cuda",
+                          dtype=torch.uint8)
+    half = cache.shape[2] // 2
+    for at in (half, 2 * half):      # scale bytes of 2^-3 .. 2^0 so that softmax is neither flat nor a single key
+        cache[:, :, at - P * D // 16:at] = torch.randint(32, 56, (n_pages, Hkv, P * D // 16), generator=g,
+                                                         device="cuda", dtype=torch.uint8)
+    start = np.concatenate(([0], np.cumsum(n))).astype(np.int32)
+    T = int(start[-1]) + 1
+    q = torch.randn(T, Hq, D, generator=g, device="cuda").bfloat16()
+    out = torch.full_like(q, 7.0)
+    ws = _ws(_lib.dspark_cache_attention_workspace_size(B, Hq, Hkv, D))
+    _lib.dspark_cache_attention(q, cache, table, _i32(start), _i32(kv), P, D ** -0.5, window, ws, out)
+    assert _lib.dspark_get_device_status(ws) == 0 and (out[-1] == 7.0).all()
+    grid = torch.tensor(np.concatenate((oc.GRID, -oc.GRID)), device="cuda")
+    e4m3 = torch.tensor(np.concatenate((oc.E4M3, oc.E4M3)), device="cuda")
+    grp, m = Hq // Hkv, torch.finfo(torch.float64).min
+    for b in range(B):
+        if n[b] == 0:
+            continue
+        rec = cache[table[b, : -(-int(kv[b]) // P)].long()]
+        kvs = []
+        for part in (0, 1):
+            r = rec[:, :, part * half:(part + 1) * half]
+            c = r[:, :, :P * D // 2].reshape(-1, Hkv, D // 32, P, 16)
+            v = grid[torch.stack((c & 15, c >> 4), -1).int()].permute(1, 0, 3, 2, 4, 5).reshape(Hkv, -1, D // 16, 16)
+            s = e4m3[r[:, :, P * D // 2:].int()].reshape(-1, Hkv, P, D // 16).transpose(0, 1).reshape(Hkv, -1, D // 16, 1)
+            kvs.append((v * s).reshape(Hkv, -1, D)[:, : kv[b]])
+        K, V = kvs
+        x = torch.einsum("nhgd,hsd->nhgs", q[start[b]:start[b + 1]].double().reshape(n[b], Hkv, grp, D), K) * D ** -0.5
+        i = torch.arange(n[b], device="cuda")[:, None] + int(kv[b] - n[b])
+        key = torch.arange(int(kv[b]), device="cuda")
+        hide = (key > i) | ((key <= i - window) if window else torch.zeros_like(key > i))
+        p = torch.softmax(x.masked_fill(hide[:, None, None], m), -1)
+        ref = torch.einsum("nhgs,hsd->nhgd", p, V).reshape(n[b], Hq, D)
+        mean = torch.einsum("nhgs,hsd->nhgd", p, V.abs()).reshape(n[b], Hq, D)
+        # P's rounding (2^-11, twice), scores of D products in fp32 (|q||k| * scale * D * 2^-23, twice), exp2 and sums
+        size = (q[start[b]:start[b + 1]].double().norm(dim=-1).max() * K.norm(dim=-1).max() * D ** -0.5).item()
+        lim = mean * (2.0 ** -10 + 2 * D * 2.0 ** -23 * size + 2.0 ** -19 + len(key) * 2.0 ** -23) + \
+            len(key) * 2.0 ** -24 * V.abs().max() * p.amax(-1).reshape(n[b], Hq, 1)
+        err = (out[start[b]:start[b + 1]].double() - ref).abs()
+        assert (err <= lim * (1 + 2.0 ** -7) + ref.abs() * 2.0 ** -8).all(), (b, n[b], kv[b], err.max().item())
+
+
 @pytest.mark.parametrize("gain", [1e-30, 1e-3, 300.0, 1e30])
 def test_attention_query_sizes(gain):
     """Queries far outside f16's range, and scores that grow along the context so that the running maximum rises."""
