@@ -134,7 +134,7 @@ struct AttnArgs {
     int32_t *desc;   // per CTA: the item it leaves unfinished
     float2 *part_ml;
     float *part_o;
-    long long budget;
+    uint32_t polls;   // bound of every wait
 };
 size_t attention_ws_bytes(int D);
 // Tiles of 128 keys a call can need at most; the kernel adds up their costs

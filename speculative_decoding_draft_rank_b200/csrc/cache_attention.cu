@@ -6,27 +6,29 @@
 // (max(0, p_r - window + 1) <= i <= p_r):
 //   x_i = qk_mul * <q_r, k_i>,  o_r = sum_i 2^(x_i - m) v_i / sum_i 2^(x_i - m).
 //
-// All rows of one request and key head (n_b * group, in blocks of 64) share
-// one pass over its keys: an item.  Items are cut into tiles of 128 keys, the
-// tiles of all items are laid end to end, and every CTA takes an equal run of
-// them, so ragged lengths and single long requests load the machine evenly.
-// An item that a CTA does not finish leaves (m, sum, o) in the workspace, and
-// a second kernel joins its parts in a fixed order.
+// All rows of one request and key head (n_b * group, in equal blocks of at
+// most 48) share one pass over its keys: an item.  Items are cut into tiles of
+// 128 keys, the costs of all tiles are laid end to end, and every CTA takes an
+// equal run of them, so ragged lengths and single long requests load the
+// machine evenly.  An item that a CTA does not finish leaves (m, sum, o) in
+// the workspace, and a second kernel joins its parts in a fixed order.
 //
-// Keys are the M = 128 side of both products, so a tile costs little more for
-// one query row than for 64:
+// Keys are the M = 128 side of both products, so that a tile costs little
+// more for 48 query rows than for one (measured: an MMA with M = 128 and both
+// operands in shared memory takes 39 cycles for 16 columns and 48 for 64; with
+// A in TMEM 9 and 32):
 //   S^T [keys x rows] = K Q^T      A = K in TMEM, B = Q in shared memory
 //   O^T [D x rows]   += V^T P^T    A = V in shared memory, B = P
 //   L   [.. x rows]  += 1 P^T      A = ones in TMEM: the softmax sums, of the
 //                                  rounded P that the products use
 // Three groups of four warps take the tiles in turn, and a group does all of
-// a tile's arithmetic, a thread per key: its K codes into f16 in TMEM, the
-// probabilities of all rows when the scores are there, its V codes into f16 in
-// shared memory; the group that ends an item writes its result.  So a tile
-// costs a warp six waits, and while one group waits for its products the
-// others work.  (With a role per step -- keys, values, softmax in 24 warps --
-// the waits and hand-overs were half of all instructions, and a tile took
-// 1700 cycles.)  Four more warps:
+// a tile's arithmetic, a thread per key: its K codes into f16 in TMEM (a tile
+// of its own ahead, so that the scores are there when it needs them), the
+// probabilities of all rows, its V codes into f16 in shared memory; the group
+// that ends an item writes its result.  So a tile costs a warp six waits, and
+// while one group waits the others work.  (With a role per step -- keys,
+// values, softmax in 24 warps -- waits and hand-overs were half of all
+// instructions.)  Four more warps:
 //   12  pages: the tiles' record addresses from the block table, ahead of use
 //   13  issues the score MMAs
 //   14  issues the MMAs with the values and the ones
@@ -40,6 +42,14 @@
 // (and O, L rescaled) when a score passes it by more than 8, so P <= 256 and
 // f16 keeps its 11 bits; K, V and Q (scaled by a power of two per row) are
 // exact in f16, so P's rounding is the only one before the output's.
+//
+// Measured: 1450-1900 cycles a tile (18 KB of cache) where HBM would need 800.
+// A tile moves 1200 (32 rows) to 1350 (48 rows) x 128 bytes through shared
+// memory -- copies, codes, V as f16 in and out, P, the row constants -- and
+// takes 700 instructions of every warp, three of which share a scheduler; the
+// two together bound it, and reading 64 pages from L2 only is 3-5 % faster.
+// The code has to stay small: with slow paths and unrolled loops laid out
+// differently, and nothing else changed, the same case took 347 to 511 us.
 // Every wait is bounded: on expiry the roles run on without waiting, nothing
 // more is copied or multiplied, and the status word says so.
 #include "cache.cuh"
@@ -158,6 +168,7 @@ struct Spot {
 __device__ __forceinline__ Spot spot_at(const AttnArgs &a, const int *cost, const int *tiles, int pos) {
     Spot p;
     int lo = 0, hi = a.B;                // the request: cost[b] <= pos < cost[b + 1]
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cost[mid] <= pos) lo = mid; else hi = mid;
@@ -166,6 +177,7 @@ __device__ __forceinline__ Spot spot_at(const AttnArgs &a, const int *cost, cons
     p.q = load_req(a, lo);
     int off = pos - cost[lo], c = 0;
     p.tiles = tiles[lo];
+#pragma unroll 1
     for (p.rb = 0;; ++p.rb) {
         p.k = row_block(a, p.q, p.rb);
         c = item_cost(p.k);
@@ -197,6 +209,7 @@ struct Walk {
                 ++rb;
             } else {
                 rb = 0;
+#pragma unroll 1
                 do q = load_req(a, ++b); while (q.n == 0 && b + 1 < a.B);
             }
             k = row_block(a, q, rb);
@@ -257,51 +270,27 @@ __device__ __forceinline__ float warp_max_f32(float v) {
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-// Bounded wait of a whole warp (converged again afterwards).  The warps of a
-// CTA wait most of the time, and a polling warp takes issue slots from the
-// ones that work: a wait that does not succeed at once sleeps up to the hint
-// (ns) at a time.  Budgets shorter than such a sleep are polled.  The slow
-// part is a function: the roles' code together has to fit the instruction
-// cache.
-__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+// Bounded waits.  The roles' code together has to fit the instruction cache,
+// so a wait is one short polling loop, and its bound a number of polls (one
+// takes some 50 cycles).  Returns false when it ran out, here or in another
+// role.
+constexpr int kPollCycles = 32;
+__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t polls) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n, a;\n\tmov.u32 n, %4;\nPOLL%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE%=;\n\t"
+        "ld.volatile.shared.u32 a, [%3];\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t"
+        "setp.eq.and.u32 q, a, 0, q;\n\t@q bra POLL%=;\n\tst.volatile.shared.u32 [%3], 1;\nDONE%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(const_cast<int *>(abort))), "r"(polls)
         : "memory");
     return ok != 0;
 }
-// Returns false when the wait ran out, here or in another role.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, long long budget) {
-    const long long t0 = clock64();
-    for (;;) {
-        uint32_t ok, stop;
-        if (budget >= 1000000)
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 32;\nTRY%=:\n\t"
-                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE%=;\n\tsub.u32 n, n, 1;\n\t"
-                "setp.ne.u32 q, n, 0;\n\t@q bra TRY%=;\nDONE%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(bar), "r"(parity)
-                : "memory");
-        else
-            ok = bar_done(bar, parity);
-        if (ok) return true;
-        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort) : "memory");
-        if (stop) return false;
-        if (clock64() - t0 > budget) {
-            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1) : "memory");
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
-    return bar_done(smem_u32(bar), parity) ||
-           wait_slow(smem_u32(bar), parity, smem_u32(const_cast<int *>(abort)), budget);
-}
-__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long budget) {
-    wait1(bar, parity, abort, budget);
+// The same for a whole warp, converged again afterwards.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t polls) {
+    wait1(bar, parity, abort, polls);
     __syncwarp();
 }
 // The 128 threads of softmax group sg.
@@ -428,11 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int sum = 0, sum_t = 0;
     bool bad = false;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const Req q = load_req(a, b);
         bad |= __ldg(a.kv_len + b) != q.L || __ldg(a.q_start + b) != q.q0 || __ldg(a.q_start + b + 1) != q.q0 + q.n;
         prefix[b] = sum;
         before_t[b] = sum_t;
+#pragma unroll 1
         for (int rb = 0; rb < row_blocks(a, q); ++rb) {
             const Block k = row_block(a, q, rb);
             sum += item_cost(k) * a.Hkv;
@@ -452,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     if (lane == 31) ms.scan[warp] = make_int2(inc, inc_t);
     if (tid == 0) {
         ms.abort = 0;
+#pragma unroll 1
         for (int i = 0; i < kAhead; ++i) {
             mbar_init(&ms.rec_full[i], 1);
             mbar_init(&ms.rec_empty[i], 4);
@@ -475,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     }
     __syncthreads();
     int before = inc - sum, total = 0, before_tiles = inc_t - sum_t, all_tiles = 0;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
         const int2 x = ms.scan[w];
         if (w < warp) {
@@ -484,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         total += x.x;
         all_tiles += x.y;
     }
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         prefix[b] += before;
         before_t[b] += before_tiles;
@@ -531,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
             unsigned long long r = 0;
             if (x < tiles) {
                 // Only what the producer has published is an address.
-                if (wait1(&ms.rec_full[x % kAhead], (x / kAhead) & 1, abort, a.budget)) r = ms.rec[x % kAhead][key / a.P];
+                if (wait1(&ms.rec_full[x % kAhead], (x / kAhead) & 1, abort, a.polls)) r = ms.rec[x % kAhead][key / a.P];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.rec_empty[x % kAhead]);
             }
@@ -550,18 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         // The keys go into the group's TMEM buffer one own tile ahead, so the
         // scores are there when the tile's turn comes.
         auto unpack_keys = [&]() {
-            uint4 codes[D / 32];
-            uint32_t sc[D / 64];
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) sc[c] = *reinterpret_cast<const uint32_t *>(kscale + c * 4);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) codes[c] = *reinterpret_cast<const uint4 *>(kraw + c * (kTile * 16));
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; c += 2) {   // 64 dims: two pieces of codes, one word of scales
+                const uint32_t sc = *reinterpret_cast<const uint32_t *>(kscale + c * 2);
+                const uint4 c0 = *reinterpret_cast<const uint4 *>(kraw + c * (kTile * 16));
+                const uint4 c1 = *reinterpret_cast<const uint4 *>(kraw + (c + 1) * (kTile * 16));
                 uint32_t r[16];
-                if (c & 1) unpack32(codes[c], scale_f16x2<2>(sc[c / 2]), scale_f16x2<3>(sc[c / 2]), r);
-                else unpack32(codes[c], scale_f16x2<0>(sc[c / 2]), scale_f16x2<1>(sc[c / 2]), r);
+                unpack32(c0, scale_f16x2<0>(sc), scale_f16x2<1>(sc), r);
                 tmem_st16(tm + lane_base + kColK + sg * 64 + c * 16, r);
+                unpack32(c1, scale_f16x2<2>(sc), scale_f16x2<3>(sc), r);
+                tmem_st16(tm + lane_base + kColK + sg * 64 + c * 16 + 16, r);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -587,15 +579,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         uint32_t ph = 0;       // parity of this group's barriers for its current tile
         int end = 0;           // the piece's tiles are [.., end) of the run
         g = sg;
+#pragma unroll 1
         for (int piece = 0; end < tiles; ++piece) {
             Rows &rw = ms.rows[piece & 1];
-            wait(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
+            wait(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.polls);
             if (soft_any(sg, *abort != 0)) break;   // the piece may not be there: the four warps leave together
             const int nr = rw.nr, N = (nr + 15) / 16 * 16, t0 = rw.t0, t1 = rw.t1, g0 = end;
             // Tiles that every row sees whole need no mask.
             const int all_hi = rw.lim[0].y, all_lo = rw.lim[nr - 1].x;
             int version = 0;
             end += t1 - t0;
+#pragma unroll 1
             for (; g < end; g += kGroups) {
                 const int t = t0 + g - g0;
                 const int ri = g % kRing, kpos = rw.base + t * kTile, me = kpos + key;
@@ -604,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                 uint8_t *prow = sm + Y::p + ri * Y::kPBytes + key * 128;
                 const bool masked = kpos + kTile > all_hi || kpos < all_lo;
                 // Probabilities.
-                wait(&ms.pv_done[ri], rp ^ 1, abort, a.budget);      // of tile g - kRing: it read this P buffer
-                wait(&ms.s_full[sg], ph, abort, a.budget);
+                wait(&ms.pv_done[ri], rp ^ 1, abort, a.polls);      // of tile g - kRing: it read this P buffer
+                wait(&ms.s_full[sg], ph, abort, a.polls);
                 tc_fence_after();
                 if (t == t0) {
                     // The rows' first maxima: a quarter of the rows a warp, over
@@ -631,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.m_full[piece & 1]);
                 }
-                if (t < t0 + kGroups) wait(&ms.m_full[piece & 1], (piece >> 1) & 1, abort, a.budget);
+                if (t < t0 + kGroups) wait(&ms.m_full[piece & 1], (piece >> 1) & 1, abort, a.polls);
                 bool raise = false, mine = t == t0, have_v = false;   // mine: tile g - 1 had its turn (or is another item's)
                 for (;;) {
                     if (raise) {
@@ -668,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                         ++version;
                         soft_sync(sg);
                         if (t > t0) {
-                            wait(&ms.pv_done[(g - 1) % kRing], ((g - 1) / kRing) & 1, abort, a.budget);
+                            wait(&ms.pv_done[(g - 1) % kRing], ((g - 1) / kRing) & 1, abort, a.polls);
                             tc_fence_after();
 #pragma unroll 1
                             for (int r0 = 0; r0 < N; r0 += 4) {
@@ -690,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     }
                     float top = -INFINITY;
                     if (masked) {   // rare: one code for every number of rows
+#pragma unroll 1
                         for (int c = 0; c < N; c += 16)
                             top = fmaxf(top, probs<1, true>(ts, rw, prow, c, key, me));
                     } else {
@@ -714,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c)
                             codes[c] = *reinterpret_cast<const uint4 *>(vraw + c * (kTile * 16));
-                        if (g >= 2) wait(&ms.pv_done[(g - 2) % kRing], ((g - 2) / kRing) & 1, abort, a.budget);
+                        if (g >= 2) wait(&ms.pv_done[(g - 2) % kRing], ((g - 2) / kRing) & 1, abort, a.polls);
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t r[16];
@@ -732,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     }
                     if (!mine) {
                         mine = true;
-                        wait(&ms.turn[p1], ph ^ x1, abort, a.budget);
+                        wait(&ms.turn[p1], ph ^ x1, abort, a.polls);
                         const int v = __shfl_sync(0xffffffffu, rw.version, 0);
                         if (v != version) {
                             version = v;
@@ -743,58 +738,76 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                     raise = soft_any(sg, top > kRaise);
                     if (!raise) break;
                 }
-                if (t == t0 && g > 0) wait(&ms.turn[p1], ph ^ x1, abort, a.budget);   // the last item's O was read
+                if (t == t0 && g > 0) wait(&ms.turn[p1], ph ^ x1, abort, a.polls);   // the last item's O was read
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.vp_full[ri]);
                 if (t + 1 == t1) {
                     // The piece's result: this thread's dim of every row.
-                    wait(&ms.pv_done[ri], rp, abort, a.budget);
+                    wait(&ms.pv_done[ri], rp, abort, a.polls);
                     tc_fence_after();
                     const bool whole = t0 == 0 && t1 == rw.nt;
                     const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-                    // O is read and its place given back before the results are stored.
-                    uint32_t y[kRows / 2];
+                    if (whole) {
+                        // O is read and its place given back before the results are stored.
+                        uint32_t y[kRows / 2];
 #pragma unroll
-                    for (int c = 0; c < kRows / 16; ++c) {
-                        if (c * 16 >= nr) break;
-                        __syncwarp();
-                        uint32_t o[16], l[16];
-                        tmem_ld16(tm + lane_base + kColO + c * 16, o);
-                        tmem_ld16(tm + lane_base + kColL + c * 16, l);
-                        tmem_ld_wait();
-                        if (whole) {
+                        for (int c = 0; c < kRows / 16; ++c) {
+                            if (c * 16 < nr) {
+                                __syncwarp();
+                                uint32_t o[16], l[16];
+                                tmem_ld16(tm + lane_base + kColO + c * 16, o);
+                                tmem_ld16(tm + lane_base + kColL + c * 16, l);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                // No visible key: the sum is 0 and so is O.
-                                const float l0 = __uint_as_float(l[i]), l1 = __uint_as_float(l[i + 1]);
-                                const float v0 = l0 == 0.f ? 0.f : rcp(l0) * a.v_mul, v1 = l1 == 0.f ? 0.f : rcp(l1) * a.v_mul;
-                                const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(o[i]) * v0,
-                                                                               __uint_as_float(o[i + 1]) * v1);
-                                y[c * 8 + i / 2] = *reinterpret_cast<const uint32_t *>(&z);
+                                for (int i = 0; i < 16; i += 2) {
+                                    // No visible key: the sum is 0 and so is O.
+                                    const float l0 = __uint_as_float(l[i]), l1 = __uint_as_float(l[i + 1]);
+                                    const float v0 = l0 == 0.f ? 0.f : rcp(l0) * a.v_mul;
+                                    const float v1 = l1 == 0.f ? 0.f : rcp(l1) * a.v_mul;
+                                    const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(o[i]) * v0,
+                                                                                   __uint_as_float(o[i + 1]) * v1);
+                                    y[c * 8 + i / 2] = *reinterpret_cast<const uint32_t *>(&z);
+                                }
                             }
-                        } else {
-                            float *po = a.part_o + ((size_t)slot * kRows + c * 16) * D + key;
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.turn[sg]);
+                        if (key < D) {
+                            uint16_t *out = reinterpret_cast<uint16_t *>(a.out) + key;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int r = c * 16 + i;
-                                if (r < nr && key < D) po[i * D] = __uint_as_float(o[i]);
+                            for (int r = 0; r < kRows; r += 4) {
+                                if (r < nr) {
+                                    const int4 w = *reinterpret_cast<const int4 *>(&rw.orow[r]);
+                                    out[(long long)w.x * D] = (uint16_t)y[r / 2];
+                                    if (r + 1 < nr) out[(long long)w.y * D] = (uint16_t)(y[r / 2] >> 16);
+                                    if (r + 2 < nr) out[(long long)w.z * D] = (uint16_t)y[r / 2 + 1];
+                                    if (r + 3 < nr) out[(long long)w.w * D] = (uint16_t)(y[r / 2 + 1] >> 16);
+                                }
+                            }
+                        }
+                    } else {
+                        float *po = a.part_o + (size_t)slot * kRows * D + key;
+#pragma unroll 1
+                        for (int r0 = 0; r0 < nr; r0 += 4) {
+                            __syncwarp();
+                            uint32_t o[4], l[4];
+                            tmem_ld4(tm + lane_base + kColO + r0, o);
+                            tmem_ld4(tm + lane_base + kColL + r0, l);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = r0 + i;
+                                if (r < nr && key < D) po[r * D] = __uint_as_float(o[i]);
                                 if (r < nr && key == i)
                                     a.part_ml[slot * kRows + r] = make_float2(-rw.neg_max(r), __uint_as_float(l[i]));
                             }
                         }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.turn[sg]);
-                    if (whole && key < D) {
-#pragma unroll
-                        for (int r = 0; r < kRows; ++r) {
-                            if (r >= nr) break;
-                            const uint16_t v = (uint16_t)(r & 1 ? y[r / 2] >> 16 : y[r / 2]);
-                            reinterpret_cast<uint16_t *>(a.out)[(long long)rw.orow[r] * D + key] = v;
-                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.turn[sg]);
                     }
                     if (!whole && t0 == 0 && key == 0) {
                         int32_t *d = a.desc + blockIdx.x * kDescInts;
@@ -820,6 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         const int ppt = kTile / a.P;
         const unsigned long long rec_bytes = record_bytes(a.P, D);
         Walk wk(a, spot, tiles);
+#pragma unroll 1
         for (int t = wk.t0; g < tiles; ++g) {
             const int key0 = wk.k.base + t * kTile, np = min(ppt, max(0, (wk.k.hi - key0 + a.P - 1) / a.P));
             unsigned long long rec = 0;
@@ -833,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                       ((unsigned long long)page * a.Hkv + wk.h) * rec_bytes;
             }
             const int st = g % kAhead;
-            if (!__all_sync(0xffffffffu, wait1(&ms.rec_empty[st], ((g / kAhead) & 1) ^ 1, abort, a.budget))) break;
+            if (!__all_sync(0xffffffffu, wait1(&ms.rec_empty[st], ((g / kAhead) & 1) ^ 1, abort, a.polls))) break;
             if (lane < 8) ms.rec[st][lane] = rec;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.rec_full[st]);
@@ -843,18 +857,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         // -------------------------------------------------------- scores
         if (elect_one()) {
             const uint32_t q0 = desc_lo(smem_u32(sm + Y::q), 16);
+#pragma unroll 1
             for (int piece = 0; g < tiles; ++piece) {
-                if (!wait1(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget)) break;
+                if (!wait1(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.polls)) break;
                 const Rows &rw = ms.rows[piece & 1];
                 const int g_end = g + rw.t1 - rw.t0;
                 const uint32_t id = idesc_f16((rw.nr + 15) / 16 * 16, false, false);
                 const uint32_t q_lo = q0 + (piece & 1) * (Y::kQBytes / 16);
                 bool ok = true;
+#pragma unroll 1
                 for (; g < g_end; ++g) {
                     const int sg = g % kGroups, ri = g % kRing;
                     // The keys are there, and the scores of tile g - kRing are done with.
-                    ok = wait1(&ms.k_full[sg], (g / kGroups) & 1, abort, a.budget) &&
-                         wait1(&ms.vp_full[ri], ((g / kRing) & 1) ^ 1, abort, a.budget);
+                    ok = wait1(&ms.k_full[sg], (g / kGroups) & 1, abort, a.polls) &&
+                         wait1(&ms.vp_full[ri], ((g / kRing) & 1) ^ 1, abort, a.polls);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t ds = tm + kColS + ri * kRows, dk = tm + kColK + sg * 64;
@@ -873,15 +889,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         if (elect_one()) {
             const uint32_t v0 = desc_lo(smem_u32(sm + Y::v), D == 128 ? kTile * 128 : 0);
             const uint32_t p0 = desc_lo(smem_u32(sm + Y::p), 0);
+#pragma unroll 1
             for (int piece = 0; g < tiles; ++piece) {
-                if (!wait1(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.budget)) break;
+                if (!wait1(&ms.q_full[piece & 1], (piece >> 1) & 1, abort, a.polls)) break;
                 const Rows &rw = ms.rows[piece & 1];
                 const int N = (rw.nr + 15) / 16 * 16, g0 = g, g_end = g + rw.t1 - rw.t0;
                 const uint32_t id_o = idesc_f16(N, true, true), id_l = idesc_f16(N, false, true);
                 bool ok = true;
+#pragma unroll 1
                 for (; g < g_end; ++g) {
                     const int ri = g % kRing;
-                    ok = wait1(&ms.vp_full[ri], (g / kRing) & 1, abort, a.budget);
+                    ok = wait1(&ms.vp_full[ri], (g / kRing) & 1, abort, a.polls);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t v_lo = v0 + (g & 1) * (Y::kVBytes / 16), p_lo = p0 + ri * (Y::kPBytes / 16);
@@ -907,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
             Rows &rw = ms.rows[piece & 1];
             uint8_t *qs = sm + Y::q + (piece & 1) * Y::kQBytes;
             const int nr = wk.k.nr, N = (nr + 15) / 16 * 16;
-            wait(&ms.q_empty[piece & 1], ((piece >> 1) & 1) ^ 1, abort, a.budget);
+            wait(&ms.q_empty[piece & 1], ((piece >> 1) & 1) ^ 1, abort, a.polls);
             const __nv_bfloat16 *src[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -1073,7 +1091,7 @@ cudaError_t launch_cache_attention(AttnArgs a, void *ws, cudaStream_t st) {
     a.part_ml = reinterpret_cast<float2 *>(p);
     p += align256((size_t)2 * kMaxCtas * kRows * sizeof(float2));
     a.part_o = reinterpret_cast<float *>(p);
-    a.budget = wait_budget(kWaitBudget);
+    a.polls = (uint32_t)(wait_budget(kWaitBudget) / kPollCycles) + 1;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
