@@ -271,10 +271,11 @@ __device__ __forceinline__ float warp_max_f32(float v) {
     return r;
 }
 // Bounded waits.  The roles' code together has to fit the instruction cache,
-// so a wait is one short polling loop, and its bound a number of polls (one
-// takes some 50 cycles).  Returns false when it ran out, here or in another
-// role.
-constexpr int kPollCycles = 32;
+// so a wait is one short polling loop, and its bound a number of polls: an
+// unsatisfied try_wait suspends its warp and returns after some 7800 cycles
+// (measured; with or without a hint), so the default budget ends a wait in
+// about four seconds.  Returns false when it ran out, here or in another role.
+constexpr int kPollCycles = 4000;
 __device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t polls) {
     uint32_t ok;
     asm volatile(
