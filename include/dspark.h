@@ -393,7 +393,7 @@ dspark_status dspark_survival_auc(const float *S, const int32_t *acc, int N, int
  * Byte j of a 16-byte piece holds dims 2j (low nibble) and 2j + 1 of its
  * 32-dim chunk as e2m1; a scale byte is the e4m3 scale of 16 dims; the value
  * is code * scale * k_scale (v_scale).  The scales k_scale and v_scale belong
- * to the layer, are positive and finite, and are 1 unless values lie outside
+ * to the layer, lie in [2^-64, 2^64], and are 1 unless values lie outside
  * about [2^-9, 2688].  The cache needs no initialisation.
  * Slot of token t of a request: table[b, t / P] * P + t % P.
  * The tokens of a round are packed by request: rows q_start[b] .. q_start[b+1],
@@ -471,8 +471,9 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
 
 /* Attention of the round's tokens over the cache.  Token j of request b has
  * position p = kv_len[b] - n_b + j and sees keys max(0, p - window + 1) .. p
- * (window = 0: all up to p), scores times `scale`; query head hq reads key
- * head hq / (Hq / Hkv).  A token that sees no key gives zeros.  Rows from
+ * (window = 0: all up to p), scores times `scale` (scale * k_scale * log2(e)
+ * finite in fp32); query head hq reads key head hq / (Hq / Hkv).
+ * A token that sees no key gives zeros.  Rows from
  * q_start[B] on are left alone.
  * Inputs:  q [T, Hq, D] bf16, tokens q_stride elements apart as above; table
  *          [B, max_pages], q_start [B+1], kv_len [B] as dspark_cache_plan

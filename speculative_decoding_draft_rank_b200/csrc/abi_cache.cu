@@ -16,7 +16,8 @@ bool table_ok(int B, int P, int max_pages, int n_pages) {
            (long long)n_pages * P <= 0x7fffffffLL && (long long)max_pages * P <= (1LL << 30);
 }
 bool heads_ok(int Hq, int Hkv) { return Hkv >= 1 && Hq >= Hkv && Hq <= 1024 && Hq % Hkv == 0; }
-bool gain_ok(float g) { return g > 0.f && std::isfinite(g); }
+// 6 g, 512 * 6 g and their reciprocals stay normal fp32 numbers.
+bool gain_ok(float g) { return g >= 0x1p-64f && g <= 0x1p64f; }
 // Rows are read in 16-byte pieces: base and token stride on 16-byte boundaries,
 // the stride at least the token's heads.
 bool rows_ok(const void *p, long long stride, int heads, int D, int dtype) {
@@ -120,7 +121,7 @@ dspark_status dspark_cache_attention(const void *q, long long q_stride, const vo
     if (dspark_status s = injected("dspark_cache_attention")) return s;
     if (dtype != DSPARK_BF16) return DSPARK_ERR_UNSUPPORTED_DTYPE;
     if (!table_ok(B, P, max_pages, n_pages) || T < 0 || T > (1 << 24) || !heads_ok(Hq, Hkv) || !cache_dim_ok(D) ||
-        window < 0 || !std::isfinite(scale) || !gain_ok(k_scale) || !gain_ok(v_scale) ||
+        window < 0 || !gain_ok(k_scale) || !gain_ok(v_scale) || !std::isfinite(scale * k_scale * kLog2e) ||
         (long long)T * Hq > 0x7fffffffLL)
         return DSPARK_ERR_INVALID_ARG;
     if (!q || !cache || !table || !q_start || !kv_len || !out || !rows_ok(q, q_stride, Hq, D, dtype) ||

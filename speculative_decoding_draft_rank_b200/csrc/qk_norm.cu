@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) qk_norm_rope_kernel(const Norm
         load8(wkb, static_cast<const T *>(a.wk) + db);
     }
     for (int f = threadIdx.x; f < a.rot / 2; f += blockDim.x) {
-        // The angle in half turns, less whole turns, in fp64 (the product is exact).
+        // The angle in half turns, less whole turns, in fp64.
         const double x = (double)pos * (double)__ldg(a.inv_freq + f) * 0.15915494309189533577;
         float s, c;
         sincospif((float)(2.0 * (x - rint(x))), &s, &c);

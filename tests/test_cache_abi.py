@@ -130,3 +130,17 @@ def test_binding_refuses_host_tensors_and_wrong_types(lib):
     with pytest.raises(ValueError):
         _lib.dspark_cache_attention(q, torch.zeros(4, 2, 99, dtype=torch.uint8), torch.zeros(1, 4, dtype=torch.int32),
                                     i[:2], i[:1], 16, 0.1, 0, ws, q)
+
+
+@pytest.mark.parametrize("g", [2.0 ** -65, 1e-40, 2.0 ** 65, 3e38])
+def test_layer_scales_out_of_range(lib, g):
+    """Their reciprocals and products leave fp32's normal range."""
+    assert _norm(lib, kg=g) == 1 and _norm(lib, vg=g) == 1
+    assert _attend(lib, kg=g) == 1 and _attend(lib, vg=g) == 1
+    assert lib.dspark_cache_read(A, A, 3, 4, 64, 16, 9, g, 1.0, 1, A, A, WS, 256, None) == 1
+    assert _norm(lib, kg=2.0 ** -64, vg=2.0 ** 64, T=0) == 0
+
+
+def test_score_scale_that_overflows(lib):
+    assert _attend(lib, scale=1e38, kg=1e3) == 1 and _attend(lib, scale=-3e38) == 1
+    assert _attend(lib, scale=1e30, kg=1e3, T=0) == 0

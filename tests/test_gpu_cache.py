@@ -222,6 +222,25 @@ def test_cache_write_of_nan_and_infinity():
     assert np.array_equal(cache.cpu().numpy(), ref)
 
 
+@pytest.mark.parametrize("e", [-64, 64])
+def test_cache_write_at_the_ends_of_the_layer_scales(e):
+    """Powers of two go through every step exactly, so x * g stored with scale g has the bytes of x."""
+    T, Hkv, D, P, g = 16, 2, 64, 16, 2.0 ** e
+    gen = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(T, Hkv, D, generator=gen).cuda() for _ in range(2))
+    slot, ws, caches = _i32(range(T)), _ws(), []
+    for s in (1.0, g):
+        cache = _cache(1, Hkv, P, D)
+        _lib.dspark_qk_norm_rope(k * s, k * s, None, None, EPS1, None, None, False, None, torch.empty_like(k), None, ws,
+                                 v=v * s, cache=cache, slot=slot, page=P, k_scale=s, v_scale=s)
+        out = torch.empty_like(k), torch.empty_like(v)
+        _lib.dspark_cache_read(cache, slot, P, *out, ws, k_scale=s, v_scale=s)
+        caches.append((cache, out[0] / s, out[1] / s))
+    assert _lib.dspark_get_device_status(ws) == 0
+    for a, b in zip(*caches):
+        assert torch.equal(a, b)
+
+
 # --------------------------------------------------------------- attention
 def _fill(rng, B, Hkv, D, P, kv_len, kg=1.0, vg=1.0):
     """A cache of garbage bytes with the tokens of every request written by the oracle."""
