@@ -74,12 +74,14 @@ dspark_status dspark_qk_norm_rope(const void *q, long long q_stride, const void 
     if (T < 0 || T > (1 << 24) || !heads_ok(Hq, Hkv) || !cache_dim_ok(D) || rot < 0 || rot > D || rot % 32 != 0 ||
         !(eps >= 0.f))
         return DSPARK_ERR_INVALID_ARG;
-    if (!q || !k || !q_out || (!k_out && !cache) || (rot > 0 && (!pos || !inv_freq))) return DSPARK_ERR_INVALID_ARG;
+    // An empty array may have no address.
+    if (T > 0 && (!q || !k || !q_out || (!k_out && !cache) || (rot > 0 && (!pos || !inv_freq))))
+        return DSPARK_ERR_INVALID_ARG;
     if (!rows_ok(q, q_stride, Hq, D, dtype) || !rows_ok(k, k_stride, Hkv, D, dtype) || !aligned16(q_out) ||
         !aligned16(k_out) || !aligned16(wq) || !aligned16(wk))
         return DSPARK_ERR_INVALID_ARG;
     if (cache != nullptr) {
-        if (!v || !slot || !page_ok(P) || n_pages < 1 || (long long)n_pages * P > 0x7fffffffLL || !gain_ok(k_scale) ||
+        if ((T > 0 && (!v || !slot)) || !page_ok(P) || n_pages < 1 || (long long)n_pages * P > 0x7fffffffLL || !gain_ok(k_scale) ||
             !gain_ok(v_scale) || !aligned16(cache) || !rows_ok(v, v_stride, Hkv, D, dtype))
             return DSPARK_ERR_INVALID_ARG;
     }
@@ -99,7 +101,7 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
     if (T < 0 || T > (1 << 24) || !heads_ok(Hkv, Hkv) || !cache_dim_ok(D) || !page_ok(P) || n_pages < 1 ||
         (long long)n_pages * P > 0x7fffffffLL || !gain_ok(k_scale) || !gain_ok(v_scale))
         return DSPARK_ERR_INVALID_ARG;
-    if (!cache || !slot || !k_out || !v_out || !aligned16(cache) || !aligned16(k_out) || !aligned16(v_out))
+    if (!cache || (T > 0 && (!slot || !k_out || !v_out)) || !aligned16(cache) || !aligned16(k_out) || !aligned16(v_out))
         return DSPARK_ERR_INVALID_ARG;
     if (dspark_status s = check_ws(ws, ws_bytes, sizeof(WsHeader))) return s;
     if (T == 0) return DSPARK_OK;
@@ -124,7 +126,7 @@ dspark_status dspark_cache_attention(const void *q, long long q_stride, const vo
         window < 0 || !gain_ok(k_scale) || !gain_ok(v_scale) || !std::isfinite(scale * k_scale * kLog2e) ||
         (long long)T * Hq > 0x7fffffffLL)
         return DSPARK_ERR_INVALID_ARG;
-    if (!q || !cache || !table || !q_start || !kv_len || !out || !rows_ok(q, q_stride, Hq, D, dtype) ||
+    if ((T > 0 && (!q || !out)) || !cache || !table || !q_start || !kv_len || !rows_ok(q, q_stride, Hq, D, dtype) ||
         !aligned16(cache) || !attention_tiles_fit(B, T, Hkv, Hq / Hkv, P, max_pages))
         return DSPARK_ERR_INVALID_ARG;
     if (dspark_status s = check_ws(ws, ws_bytes, attention_ws_bytes(D))) return s;

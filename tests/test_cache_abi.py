@@ -144,3 +144,10 @@ def test_layer_scales_out_of_range(lib, g):
 def test_score_scale_that_overflows(lib):
     assert _attend(lib, scale=1e38, kg=1e3) == 1 and _attend(lib, scale=-3e38) == 1
     assert _attend(lib, scale=1e30, kg=1e3, T=0) == 0
+
+
+def test_empty_arrays_may_have_no_address(lib):
+    assert _norm(lib, T=0, q=None, k=None, v=None, pos=None, slot=None, qo=None, ko=None) == 0
+    assert lib.dspark_cache_read(A, None, 0, 4, 64, 16, 9, 1.0, 1.0, 1, None, None, WS, 256, None) == 0
+    assert _attend(lib, T=0, q=None, out=None) == 0
+    assert _norm(lib, T=0, D=96) == 1 and _attend(lib, T=0, cache=None) == 1

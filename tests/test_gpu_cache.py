@@ -241,6 +241,19 @@ def test_cache_write_at_the_ends_of_the_layer_scales(e):
         assert torch.equal(a, b)
 
 
+def test_calls_without_tokens():
+    q, k = torch.empty(0, 4, 64, device="cuda", dtype=torch.bfloat16), torch.empty(0, 2, 64, device="cuda",
+                                                                                  dtype=torch.bfloat16)
+    cache = _cache(2, 2, 16, 64)
+    ws = _ws(_lib.dspark_cache_attention_workspace_size(1, 4, 2, 64))
+    none = _i32([])
+    _lib.dspark_qk_norm_rope(q, k, None, None, EPS1, none, torch.ones(16, device="cuda"), False, None, q, None, ws, v=k,
+                             cache=cache, slot=none, page=16)
+    _lib.dspark_cache_read(cache, none, 16, k, torch.empty_like(k), ws)
+    _lib.dspark_cache_attention(q, cache, _i32([[0]]), _i32([0, 0]), _i32([5]), 16, 0.1, 0, ws, torch.empty_like(q))
+    assert _lib.dspark_get_device_status(ws) == 0 and (cache == 255).all()
+
+
 # --------------------------------------------------------------- attention
 def _fill(rng, B, Hkv, D, P, kv_len, kg=1.0, vg=1.0):
     """A cache of garbage bytes with the tokens of every request written by the oracle."""
