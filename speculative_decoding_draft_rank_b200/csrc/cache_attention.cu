@@ -565,15 +565,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         copy(rec, kraw, kscale);
         copy(rec ? rec + hb : 0, vraw, vscale);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        if (sg < tiles) unpack_keys();
-        next = find(sg + kGroups);
-        copy(next, kraw, kscale);
-        if (sg == 0) {
+        if (sg == 0) {   // the ones: before this group's first keys, whose wait for stores covers them
             uint32_t one[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) one[i] = 0x3c003c00u;
+            __syncwarp();
             tmem_st16(tm + lane_base + kColOne, one);
         }
+        if (sg < tiles) unpack_keys();
+        next = find(sg + kGroups);
+        copy(next, kraw, kscale);
         // The group of tile g - 1, and its parity when this group's is even.
         const int p1 = (sg + kGroups - 1) % kGroups;
         const uint32_t x1 = sg < 1;

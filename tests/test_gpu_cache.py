@@ -473,3 +473,25 @@ def test_attention_wait_that_runs_out(monkeypatch):
     monkeypatch.delenv("DSPARK_WAIT_BUDGET_CYCLES")
     _lib.dspark_clear_device_status(ws)
     _check_attention(q, cache, table, [4, 1, 4], kv, 16, 0.125, ws=ws)
+
+
+@pytest.mark.parametrize("tiles", [1, 2, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_runs_of_few_tiles(D, tiles):
+    """As many equal items as CTAs: every CTA takes one item of 1, 2 or 3 tiles.  All values are 1.5 (the
+    format holds it), so numerator and denominator are sums of the same probabilities: 1.5 after rounding to bf16."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(tiles)
+    L, P = 128 * tiles - 5, 64
+    k = rng.standard_normal((L, 1, D))
+    cache = np.zeros((2 * tiles, 1, P * D // 8 * 9), np.uint8)
+    oc.write(cache, np.arange(L), k, np.full((L, 1, D), 1.5), P)
+    table = np.tile(np.arange(2 * tiles, dtype=np.int32), (sms, 1))
+    q = torch.from_numpy(rng.standard_normal((sms, 2, D))).to(torch.bfloat16).cuda()
+    ws = _ws(_lib.dspark_cache_attention_workspace_size(sms, 2, 1, D))
+    for _ in range(20):
+        out = torch.zeros_like(q)
+        _lib.dspark_cache_attention(q, torch.from_numpy(cache).cuda(), _i32(table), _i32(np.arange(sms + 1)),
+                                    _i32([L] * sms), P, D ** -0.5, 0, ws, out)
+        assert (out == 1.5).all()
+    assert _lib.dspark_get_device_status(ws) == 0
