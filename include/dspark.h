@@ -474,7 +474,8 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
  * (window = 0: all up to p), scores times `scale` (scale * k_scale * log2(e)
  * finite in fp32); query head hq reads key head hq / (Hq / Hkv).
  * A token that sees no key gives zeros.  Rows from
- * q_start[B] on are left alone.
+ * q_start[B] on are left alone.  If q_start falls anywhere nothing is written
+ * (DSPARK_DEV_LENGTH_RANGE).
  * Inputs:  q [T, Hq, D] bf16, tokens q_stride elements apart as above; table
  *          [B, max_pages], q_start [B+1], kv_len [B] as dspark_cache_plan
  *          leaves them, after the round's keys were written.

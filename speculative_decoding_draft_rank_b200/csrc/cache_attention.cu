@@ -52,6 +52,8 @@
 // differently, and nothing else changed, the same case took 347 to 511 us.
 // Every wait is bounded: on expiry the roles run on without waiting, nothing
 // more is copied or multiplied, and the status word says so.
+#include <climits>
+
 #include "cache.cuh"
 #include "tc.cuh"
 
@@ -115,7 +117,8 @@ struct Misc {
     uint64_t q_full[2], q_empty[2], m_full[2], drain[2];   // m_full: the piece's first maxima are set
     uint32_t tmem;
     int abort;
-    int2 scan[16];
+    long long scan[16];
+    int scan_t[16];
 };
 
 struct Req {
@@ -139,7 +142,7 @@ struct Block {
 __device__ __forceinline__ int row_blocks(const AttnArgs &a, const Req &q) { return (q.n * a.group + kRows - 1) / kRows; }
 __device__ __forceinline__ Block row_block(const AttnArgs &a, const Req &q, int rb) {
     Block k;
-    const int rows = q.n * a.group, nb = row_blocks(a, q);
+    const int rows = q.n * a.group, nb = max(1, row_blocks(a, q));
     k.r0 = (int)((long long)rows * rb / nb);
     k.nr = (int)((long long)rows * (rb + 1) / nb) - k.r0;
     const int jf = k.r0 / a.group, jl = (k.r0 + k.nr - 1) / a.group;
@@ -156,16 +159,18 @@ __device__ __forceinline__ Block row_block(const AttnArgs &a, const Req &q, int 
 // in a run of some 20 tiles each.  CTAs get equal costs rather than equal tiles.
 __device__ __forceinline__ int tile_cost(const Block &k) { return k.nr <= 32 ? 13 : 16; }
 constexpr int kItemCost = 70, kMinQuota = 16;   // a quota holds the start of at least one tile
+constexpr long long kRefused = 1LL << 50;
 __device__ __forceinline__ int item_cost(const Block &k) { return k.nt * tile_cost(k) + kItemCost; }
 
 // The item in which position `pos` of the batch's costs lies, its first tile
 // that starts there or later (nt: none), and the tiles of the batch before that.
 struct Spot {
-    int b, rb, h, t, start, tiles;   // start: position of the item
+    int b, rb, h, t, tiles;
+    uint32_t start;                  // position of the item, from `pos`
     Req q;
     Block k;
 };
-__device__ __forceinline__ Spot spot_at(const AttnArgs &a, const int *cost, const int *tiles, int pos) {
+__device__ __forceinline__ Spot spot_at(const AttnArgs &a, const long long *cost, const int *tiles, long long pos) {
     Spot p;
     int lo = 0, hi = a.B;                // the request: cost[b] <= pos < cost[b + 1]
 #pragma unroll 1
@@ -175,19 +180,21 @@ __device__ __forceinline__ Spot spot_at(const AttnArgs &a, const int *cost, cons
     }
     p.b = lo;
     p.q = load_req(a, lo);
-    int off = pos - cost[lo], c = 0;
+    unsigned long long rest = pos - cost[lo];
+    int c = 0;
     p.tiles = tiles[lo];
 #pragma unroll 1
     for (p.rb = 0;; ++p.rb) {
         p.k = row_block(a, p.q, p.rb);
         c = item_cost(p.k);
-        if (off < c * a.Hkv) break;
-        off -= c * a.Hkv;
+        const unsigned long long all = (unsigned long long)c * a.Hkv;
+        if (rest < all) break;
+        rest -= all;
         p.tiles += p.k.nt * a.Hkv;
     }
-    p.h = off / c;
-    off -= p.h * c;
-    p.start = pos - off;
+    p.h = (int)(rest / c);
+    const int off = (int)(rest - (unsigned long long)p.h * c);
+    p.start = 0u - off;
     const int w = tile_cost(p.k);
     p.t = min(p.k.nt, (off + w - 1) / w);
     p.tiles += p.h * p.k.nt + p.t;
@@ -198,7 +205,8 @@ __device__ __forceinline__ Spot spot_at(const AttnArgs &a, const int *cost, cons
 struct Walk {
     const AttnArgs &a;
     int left;                // tiles left in the run
-    int b, rb, h, t0, t1, start;
+    int b, rb, h, t0, t1;
+    uint32_t start;          // position of the item, from that of the run (below 2^31 + 2^28 at its last tile)
     Req q;
     Block k;
     __device__ __forceinline__ void next_item() {
@@ -210,7 +218,7 @@ struct Walk {
             } else {
                 rb = 0;
 #pragma unroll 1
-                do q = load_req(a, ++b); while (q.n == 0 && b + 1 < a.B);
+                do q = load_req(a, b = min(b + 1, a.B - 1)); while (q.n == 0 && b + 1 < a.B);
             }
             k = row_block(a, q, rb);
         }
@@ -410,13 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     uint8_t *sm = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);   // still known to be shared memory
     Misc &ms = *reinterpret_cast<Misc *>(sm + Y::misc);
     // In the probabilities' place: read for the last time before the roles begin.
-    int *prefix = reinterpret_cast<int *>(sm + Y::p), *before_t = prefix + 4096;   // costs and tiles before a request
+    long long *prefix = reinterpret_cast<long long *>(sm + Y::p);   // costs and tiles before a request
+    int *before_t = reinterpret_cast<int *>(prefix + 4096);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // Tiles of every request, and their prefix: thread t sums a run of requests.
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int sum = 0, sum_t = 0;
+    long long sum = 0;
+    int sum_t = 0;   // the batch's tiles may pass 32 bits; only differences within a CTA's run are used
     bool bad = false;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -427,21 +437,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
 #pragma unroll 1
         for (int rb = 0; rb < row_blocks(a, q); ++rb) {
             const Block k = row_block(a, q, rb);
-            sum += item_cost(k) * a.Hkv;
+            sum += (long long)item_cost(k) * a.Hkv;
             sum_t += k.nt * a.Hkv;
         }
+        if (__ldg(a.q_start + b + 1) < __ldg(a.q_start + b)) sum = kRefused;
     }
     if (bad && blockIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_LENGTH_RANGE);
-    int inc = sum, inc_t = sum_t;
+    long long inc = sum;
+    int inc_t = sum_t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_t, o);
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        const int z = __shfl_up_sync(0xffffffffu, inc_t, o);
         if (lane >= o) {
             inc += y;
             inc_t += z;
         }
     }
-    if (lane == 31) ms.scan[warp] = make_int2(inc, inc_t);
+    if (lane == 31) {
+        ms.scan[warp] = inc;
+        ms.scan_t[warp] = inc_t;
+    }
     if (tid == 0) {
         ms.abort = 0;
 #pragma unroll 1
@@ -467,16 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         fence_barrier_init();
     }
     __syncthreads();
-    int before = inc - sum, total = 0, before_tiles = inc_t - sum_t, all_tiles = 0;
+    long long before = inc - sum, total = 0;
+    int before_tiles = inc_t - sum_t, all_tiles = 0;
 #pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
-        const int2 x = ms.scan[w];
+        const long long x = ms.scan[w];
+        const int y = ms.scan_t[w];
         if (w < warp) {
-            before += x.x;
-            before_tiles += x.y;
+            before += x;
+            before_tiles += y;
         }
-        total += x.x;
-        all_tiles += x.y;
+        total += x;
+        all_tiles += y;
     }
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
@@ -484,13 +502,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
         before_t[b] += before_tiles;
     }
     __syncthreads();
-    const int quota = max(kMinQuota, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    // Offsets that fall (requests would share rows), or more work than the
+    // positions of a run can count: nothing is done.
+    const bool refused = total > (long long)gridDim.x * INT_MAX;
+    if (refused && tid == 0 && blockIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_LENGTH_RANGE);
+    const int quota = refused ? INT_MAX : max(kMinQuota, (int)((total + gridDim.x - 1) / gridDim.x));
     const long long w0 = (long long)blockIdx.x * quota, w1 = w0 + quota;
     Spot spot = {};
     int tiles = 0;
-    if (w0 < total) {
-        spot = spot_at(a, prefix, before_t, (int)w0);
-        tiles = (w1 < total ? spot_at(a, prefix, before_t, (int)w1).tiles : all_tiles) - spot.tiles;
+    if (w0 < total && !refused) {
+        spot = spot_at(a, prefix, before_t, w0);
+        tiles = (w1 < total ? spot_at(a, prefix, before_t, w1).tiles : all_tiles) - spot.tiles;
     }
     if (tiles <= 0) {   // the whole CTA: no work, nothing left unfinished
         if (tid == 0) a.desc[blockIdx.x * kDescInts] = 0;
@@ -948,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                 rw.q0 = wk.q.q0;
                 rw.r0 = wk.k.r0;
                 rw.h = wk.h;
-                rw.last = (wk.start + (wk.k.nt - 1) * tile_cost(wk.k)) / quota;
+                rw.last = blockIdx.x + (wk.start + (uint32_t)((wk.k.nt - 1) * tile_cost(wk.k))) / (uint32_t)quota;
                 rw.version = 0;
             }
 #pragma unroll 1
@@ -1067,7 +1089,7 @@ template <int D>
 cudaError_t launch_d(const AttnArgs &a, int grid, cudaStream_t st) {
     const size_t bytes = Lay<D>::misc + sizeof(Misc) + 1024;
     static_assert(Lay<D>::misc + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory of an SM");
-    static_assert(2 * 4096 * sizeof(int) <= kRing * Lay<D>::kPBytes, "the prefix of the largest batch");
+    static_assert(4096 * (sizeof(long long) + sizeof(int)) <= kRing * Lay<D>::kPBytes, "the prefix of the largest batch");
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(cache_attention_kernel<D>), bytes, done);
     if (e != cudaSuccess) return e;

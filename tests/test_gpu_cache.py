@@ -495,3 +495,19 @@ def test_attention_runs_of_few_tiles(D, tiles):
                                     _i32([L] * sms), P, D ** -0.5, 0, ws, out)
         assert (out == 1.5).all()
     assert _lib.dspark_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("start", [[0, 2, 1, 3], [0, 3, 0, 3], [3, 2, 1, 0], [0, 1, 3, -1]])
+def test_attention_refuses_row_offsets_that_fall(start):
+    """Two requests would write the same rows, and their work would not fit the sums made for T rows."""
+    rng = np.random.default_rng(11)
+    cache, table = _fill(rng, 3, 2, 64, 16, [40, 200, 40])
+    q = torch.from_numpy(rng.standard_normal((3, 4, 64))).to(torch.bfloat16).cuda()
+    ws = _ws(_lib.dspark_cache_attention_workspace_size(3, 4, 2, 64))
+    args = (torch.from_numpy(cache).cuda(), _i32(table))
+    out = torch.full_like(q, 7.0)
+    _lib.dspark_cache_attention(q, *args, _i32(start), _i32([40, 200, 40]), 16, 0.125, 0, ws, out)
+    assert _lib.dspark_get_device_status(ws) == _lib.DEV_LENGTH_RANGE
+    assert (out == 7.0).all()
+    _check_attention(q.float().cpu().numpy(), cache, table, [1, 1, 1], [40, 200, 40], 16, 0.125, extra=0,
+                     ws=_ws(ws.nbytes))
