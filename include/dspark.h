@@ -481,6 +481,10 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
  *          leaves them, after the round's keys were written.
  * Outputs: out [T, Hq, D] bf16, dense, not overlapping q
  *          (DSPARK_ERR_INVALID_ARG).
+ * Limits:  T <= 2^24, T * Hq < 2^31, and for the work that T rows over full
+ *          tables could be, Hkv * (B + T * Hq / Hkv / 48 + 1) *
+ *          (max_pages * P / 8 + 102) < 2^38 (a prompt of 2^20 tokens at 64
+ *          query heads is two thirds of it).
  * fp32 scores, maxima and sums; probabilities enter the second product in
  * f16, keys, values and queries exactly.  Any n_b and any group Hq / Hkv.
  * Deterministic.  Two launches.  bf16 only (DSPARK_ERR_UNSUPPORTED_DTYPE). */

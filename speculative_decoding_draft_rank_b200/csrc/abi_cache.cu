@@ -127,7 +127,7 @@ dspark_status dspark_cache_attention(const void *q, long long q_stride, const vo
         (long long)T * Hq > 0x7fffffffLL)
         return DSPARK_ERR_INVALID_ARG;
     if ((T > 0 && (!q || !out)) || !cache || !table || !q_start || !kv_len || !rows_ok(q, q_stride, Hq, D, dtype) ||
-        !aligned16(cache) || !attention_tiles_fit(B, T, Hkv, Hq / Hkv, P, max_pages))
+        !aligned16(cache) || !attention_work_fits(B, T, Hkv, Hq / Hkv, P, max_pages))
         return DSPARK_ERR_INVALID_ARG;
     if (dspark_status s = check_ws(ws, ws_bytes, attention_ws_bytes(D))) return s;
     if (T == 0) return DSPARK_OK;

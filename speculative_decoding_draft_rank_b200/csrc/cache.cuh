@@ -137,11 +137,12 @@ struct AttnArgs {
     uint32_t polls;   // bound of every wait
 };
 size_t attention_ws_bytes(int D);
-// Tiles of 128 keys a call can need at most; the kernel adds up their costs
-// (at most 16 a tile and 70 an item) in 32 bits.
-inline bool attention_tiles_fit(int B, int T, int Hkv, int group, int P, int max_pages) {
+// The most work a call may bring, in the kernel's units (at most 16 a tile of
+// 128 keys, 70 an item of up to 48 rows): positions inside a CTA's share are
+// 32 bits, and a share is 1/148 of this.  (About four minutes of a GPU.)
+inline bool attention_work_fits(int B, int T, int Hkv, int group, int P, int max_pages) {
     const double items = (double)Hkv * ((double)B + (double)T * group / 48.0 + 1.0);
-    return items * (16.0 * ((double)max_pages * P / 128.0 + 2.0) + 70.0) < 2.0e9;
+    return items * (16.0 * ((double)max_pages * P / 128.0 + 2.0) + 70.0) < 0x1p38;
 }
 cudaError_t launch_cache_attention(AttnArgs a, void *ws, cudaStream_t st);
 

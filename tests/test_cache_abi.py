@@ -151,3 +151,13 @@ def test_empty_arrays_may_have_no_address(lib):
     assert lib.dspark_cache_read(A, None, 0, 4, 64, 16, 9, 1.0, 1.0, 1, None, None, WS, 256, None) == 0
     assert _attend(lib, T=0, q=None, out=None) == 0
     assert _norm(lib, T=0, D=96) == 1 and _attend(lib, T=0, cache=None) == 1
+
+
+def test_attention_takes_long_prompts(lib):
+    """The shape checks come before the workspace's: 3 says that the shape passed."""
+    for ok in (dict(B=1, T=131072, Hq=64, Hkv=8, P=64, mp=2048, n=4096), dict(B=1, T=98304, Hq=64, Hkv=8, mp=1536),
+               dict(B=256, T=1 << 21, Hq=64, Hkv=8, P=128, mp=1024), dict(B=1, T=1 << 20, Hq=64, Hkv=8, P=64, mp=1 << 14),
+               dict(B=4096, T=36864, Hq=64, Hkv=8, P=64, mp=1 << 14)):
+        assert _attend(lib, **{**dict(n=1 << 20, qs=8192, ws=None, out=ctypes.c_void_p(1 << 45)), **ok}) == 3, ok
+    for bad in (dict(B=1, T=1 << 21, Hq=64, Hkv=8, P=64, mp=1 << 15), dict(B=4096, T=1 << 24, Hq=64, Hkv=8, P=128, mp=8192)):
+        assert _attend(lib, **{**dict(n=1 << 20, qs=8192, ws=None, out=ctypes.c_void_p(1 << 45)), **bad}) == 1, bad

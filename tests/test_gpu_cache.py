@@ -511,3 +511,36 @@ def test_attention_refuses_row_offsets_that_fall(start):
     assert (out == 7.0).all()
     _check_attention(q.float().cpu().numpy(), cache, table, [1, 1, 1], [40, 200, 40], 16, 0.125, extra=0,
                      ws=_ws(ws.nbytes))
+
+
+@pytest.mark.parametrize("B,n,L", [(1, 20000, 1 << 20), (64, 20000, 1 << 17)])
+def test_attention_of_a_long_prompt(B, n, L):
+    """One long prompt alone, and in a batch of other seats; the first is more work than 32-bit sums hold.  Keys are
+    zero, so all weights are equal; dim d of the values is 1.5 up to its own position and 0 behind it, so the result
+    is 1.5 times a ratio of two counts, and every sum on the way is exact in fp32."""
+    Hq, D, P, cap = 48, 64, 128, 1 << 20
+    pages = L // P
+    cut = torch.linspace(1, L, D, dtype=torch.float64).long().cuda()
+    v = (torch.arange(L, device="cuda")[:, None] < cut).to(torch.bfloat16)[:, None] * 1.5
+    k = torch.zeros_like(v)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    table = torch.zeros((B, cap // P), dtype=torch.int32, device="cuda")
+    seat = B // 2
+    table[seat, :pages] = torch.randperm(pages, generator=g, device="cuda").int()
+    t = torch.arange(L, device="cuda")
+    slot = table[seat, t // P] * P + (t % P).int()
+    cache = torch.empty((pages, 1, _lib.dspark_cache_record_bytes(P, D)), dtype=torch.uint8, device="cuda")
+    ws = _ws(_lib.dspark_cache_attention_workspace_size(B, Hq, 1, D))
+    _lib.dspark_qk_norm_rope(k, k, None, None, EPS1, None, None, False, None, torch.empty_like(k), None, ws, v=v,
+                             cache=cache, slot=slot, page=P)
+    start = _i32([0] * (seat + 1) + [n] * (B - seat))
+    kv = _i32([0] * seat + [L] + [0] * (B - seat - 1))
+    q = torch.randn(n + 3, Hq, D, generator=g, device="cuda").bfloat16()
+    out = torch.full_like(q, 7.0)
+    _lib.dspark_cache_attention(q, cache, table, start, kv, P, D ** -0.5, 0, ws, out)
+    assert _lib.dspark_get_device_status(ws) == 0
+    see = torch.arange(L - n + 1, L + 1, device="cuda")[:, None]
+    ref = (1.5 * torch.minimum(cut, see).double() / see)[:, None]
+    # the reciprocal and the product in fp32, then half a step of bf16
+    assert ((out[:n].double() - ref).abs() <= ref * (2.0 ** -8 + 2.0 ** -22)).all()
+    assert (out[n:] == 7.0).all()
