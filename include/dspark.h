@@ -426,6 +426,20 @@ dspark_status dspark_cache_plan(const int32_t *ctx, const int32_t *ell, int B, i
                                 int32_t *free_count, void *ws, size_t ws_bytes, int32_t *q_start_out,
                                 int32_t *kv_len_out, int32_t *slot_out, int32_t *pos_out, void *stream);
 
+/* The same for arrays of T rows (slot_out and pos_out [T], 0 <= T <= 2^24, G
+ * and B as above without a limit on B * (G+1)), with the lengths it granted:
+ * ell_out [B] or NULL (may be ell) = max(n_b - 1, 0), what the target pass
+ * covers and verification may use.  A request without rows (n_b = 0: an empty
+ * seat, or no page for its next token) has ell_out = 0 too; only q_start_out
+ * tells it apart, and dspark_cache_commit_round takes its results back.
+ * Requests whose rows do not all fit T get those that do
+ * (DSPARK_DEV_CACHE_FULL). */
+dspark_status dspark_cache_plan_rows(const int32_t *ctx, const int32_t *ell, int B, int G, int P, int max_pages,
+                                     int n_pages, int32_t *table, int32_t *held, const int32_t *free_list,
+                                     int32_t *free_count, int T, void *ws, size_t ws_bytes, int32_t *ell_out,
+                                     int32_t *q_start_out, int32_t *kv_len_out, int32_t *slot_out, int32_t *pos_out,
+                                     void *stream);
+
 /* After verification: ctx_out[b] = ctx[b] + nout[b] (nout: dspark_verify's
  * counts, at most the planned n_b), and the pages behind those tokens go back
  * on the free list, so that committing nothing after a plan restores it.
@@ -436,6 +450,16 @@ dspark_status dspark_cache_commit(const int32_t *ctx, const int32_t *q_start, co
                                   const int32_t *done, int B, int P, int max_pages, int n_pages, int32_t *table,
                                   int32_t *held, int32_t *free_list, int32_t *free_count, void *ws, size_t ws_bytes,
                                   int32_t *ctx_out, void *stream);
+
+/* dspark_cache_commit for a round whose verification ran over every request
+ * on the lengths of dspark_cache_plan_rows: a request without rows was not
+ * seen by the target, so it emits nothing.  Its nout [B] and acc [B] become 0
+ * and its tokens [B, G+1] -1 (in place; acc and tokens may be NULL); G <= 2^20. */
+dspark_status dspark_cache_commit_round(const int32_t *ctx, const int32_t *q_start, int32_t *nout, int32_t *acc,
+                                        int32_t *tokens, const int32_t *done, int B, int G, int P, int max_pages,
+                                        int n_pages, int32_t *table, int32_t *held, int32_t *free_list,
+                                        int32_t *free_count, void *ws, size_t ws_bytes, int32_t *ctx_out,
+                                        void *stream);
 
 /* Norm, rotation and cache write of a layer's projections, in one pass.
  *   y = x / sqrt(mean(x^2) + eps) * w per query and key head (wq, wk [D]

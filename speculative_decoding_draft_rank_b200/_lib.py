@@ -36,7 +36,8 @@ EXPORTS = ("dspark_version", "dspark_draft_workspace_size", "dspark_draft_markov
            "dspark_draft_noalloc_device_status", "dspark_draft_rnn", "dspark_verify_rnn", "dspark_get_near_ties",
            "dspark_exp2_fma", "dspark_gather_admitted_targets", "dspark_cache_record_bytes", "dspark_cache_plan",
            "dspark_cache_commit", "dspark_qk_norm_rope", "dspark_cache_read",
-           "dspark_cache_attention_workspace_size", "dspark_cache_attention")
+           "dspark_cache_attention_workspace_size", "dspark_cache_attention", "dspark_cache_plan_rows",
+           "dspark_cache_commit_round")
 
 
 class DsparkError(RuntimeError):
@@ -110,6 +111,10 @@ def load() -> ctypes.CDLL:
     lib.dspark_cache_plan.argtypes = [_vp] * 2 + [_i] * 5 + [_vp] * 5 + [_sz] + [_vp] * 5
     lib.dspark_cache_commit.restype = _i
     lib.dspark_cache_commit.argtypes = [_vp] * 4 + [_i] * 4 + [_vp] * 5 + [_sz] + [_vp] * 2
+    lib.dspark_cache_plan_rows.restype = _i
+    lib.dspark_cache_plan_rows.argtypes = [_vp] * 2 + [_i] * 5 + [_vp] * 4 + [_i, _vp, _sz] + [_vp] * 6
+    lib.dspark_cache_commit_round.restype = _i
+    lib.dspark_cache_commit_round.argtypes = [_vp] * 6 + [_i] * 5 + [_vp] * 5 + [_sz] + [_vp] * 2
     lib.dspark_qk_norm_rope.restype = _i
     lib.dspark_qk_norm_rope.argtypes = ([_vp, _ll] * 3 + [_vp] * 2 + [_f] + [_vp] * 2 + [_i] * 2 + [_vp] + [_i] * 5 +
                                         [_vp] * 4 + [_i] * 2 + [_f] * 2 + [_vp, _sz, _vp])
@@ -394,6 +399,21 @@ def dspark_cache_plan(ctx, ell, G, table, held, free_list, free_count, page, ws,
             _ints(slot_out, dev, T, "slot_out"), _ints(pos_out, dev, T, "pos_out"))
 
 
+def dspark_cache_plan_rows(ctx, ell, G, table, held, free_list, free_count, page, ws, q_start_out, kv_len_out, slot_out,
+                           pos_out, ell_out=None, stream=None):
+    """dspark_cache_plan for arrays slot_out and pos_out of any number of rows;
+    ell_out [B] (may be ell) gets the admitted lengths that the plan covers."""
+    dev = _device_of(table)
+    B, max_pages = table.shape
+    T = slot_out.numel()
+    _launch("dspark_cache_plan_rows", dev, stream, _ints(ctx, dev, B, "ctx"), _ints(ell, dev, B, "ell"), B, int(G),
+            int(page), max_pages, free_list.numel(), _ints(table, dev, 1, "table"), _ints(held, dev, B, "held"),
+            _ints(free_list, dev, 1, "free_list"), _ints(free_count, dev, 1, "free_count"), T, _dense(ws, dev),
+            ws.nbytes, None if ell_out is None else _ints(ell_out, dev, B, "ell_out"),
+            _ints(q_start_out, dev, B + 1, "q_start_out"), _ints(kv_len_out, dev, B, "kv_len_out"),
+            _ints(slot_out, dev, T, "slot_out"), _ints(pos_out, dev, T, "pos_out"))
+
+
 def dspark_cache_commit(ctx, q_start, nout, done, table, held, free_list, free_count, page, ws, ctx_out,
                         stream=None):
     """After verification: ctx_out = ctx + nout (-1 where done [B], or None,
@@ -406,6 +426,22 @@ def dspark_cache_commit(ctx, q_start, nout, done, table, held, free_list, free_c
             max_pages, free_list.numel(), _ints(table, dev, 1, "table"), _ints(held, dev, B, "held"),
             _ints(free_list, dev, 1, "free_list"), _ints(free_count, dev, 1, "free_count"), _dense(ws, dev),
             ws.nbytes, _ints(ctx_out, dev, B, "ctx_out"))
+
+
+def dspark_cache_commit_round(ctx, q_start, nout, acc, tokens, done, table, held, free_list, free_count, page, ws,
+                              ctx_out, stream=None):
+    """dspark_cache_commit after a round's verification: requests without
+    planned rows emit nothing (nout and acc [B] become 0, tokens [B, G+1] -1,
+    in place; acc and tokens may be None)."""
+    dev = _device_of(table)
+    B, max_pages = table.shape
+    G = 0 if tokens is None else tokens.shape[1] - 1
+    _launch("dspark_cache_commit_round", dev, stream, _ints(ctx, dev, B, "ctx"), _ints(q_start, dev, B + 1, "q_start"),
+            _ints(nout, dev, B, "nout"), None if acc is None else _ints(acc, dev, B, "acc"),
+            None if tokens is None else _ints(tokens, dev, B * (G + 1), "tokens"),
+            None if done is None else _ints(done, dev, B, "done"), B, G, int(page), max_pages, free_list.numel(),
+            _ints(table, dev, 1, "table"), _ints(held, dev, B, "held"), _ints(free_list, dev, 1, "free_list"),
+            _ints(free_count, dev, 1, "free_count"), _dense(ws, dev), ws.nbytes, _ints(ctx_out, dev, B, "ctx_out"))
 
 
 def dspark_qk_norm_rope(q, k, wq, wk, eps, pos, inv_freq, interleaved, n_rows, q_out, k_out, ws, v=None, cache=None,

@@ -25,6 +25,24 @@ bool rows_ok(const void *p, long long stride, int heads, int D, int dtype) {
     return aligned16(p) && stride >= (long long)heads * D && stride % per == 0;
 }
 
+dspark_status plan(const PlanArgs &a, size_t ws_bytes, void *stream) {
+    if (!table_ok(a.B, a.P, a.max_pages, a.n_pages) || a.G < 0 || a.G > (1 << 20) || a.T < 0 || a.T > (1 << 24))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!a.ctx || !a.ell || !a.table || !a.held || !a.free_list || !a.free_count || !a.q_start || !a.kv_len ||
+        (a.T > 0 && (!a.slot || !a.pos)))
+        return DSPARK_ERR_INVALID_ARG;
+    if (dspark_status s = check_ws(a.hdr, ws_bytes, sizeof(WsHeader))) return s;
+    return cuda_status(launch_cache_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+dspark_status commit(const CommitArgs &a, size_t ws_bytes, void *stream) {
+    if (!table_ok(a.B, a.P, a.max_pages, a.n_pages) || a.G < 0 || a.G > (1 << 20)) return DSPARK_ERR_INVALID_ARG;
+    if (!a.ctx || !a.q_start || !a.nout || !a.table || !a.held || !a.free_list || !a.free_count || !a.ctx_out)
+        return DSPARK_ERR_INVALID_ARG;
+    if (dspark_status s = check_ws(a.hdr, ws_bytes, sizeof(WsHeader))) return s;
+    return cuda_status(launch_cache_commit(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -38,15 +56,22 @@ dspark_status dspark_cache_plan(const int32_t *ctx, const int32_t *ell, int B, i
                                 int32_t *free_count, void *ws, size_t ws_bytes, int32_t *q_start_out,
                                 int32_t *kv_len_out, int32_t *slot_out, int32_t *pos_out, void *stream) {
     if (dspark_status s = injected("dspark_cache_plan")) return s;
-    if (!table_ok(B, P, max_pages, n_pages) || G < 0 || G > (1 << 20) || (long long)B * (G + 1) > (1 << 24))
-        return DSPARK_ERR_INVALID_ARG;
-    if (!ctx || !ell || !table || !held || !free_list || !free_count || !q_start_out || !kv_len_out || !slot_out ||
-        !pos_out)
-        return DSPARK_ERR_INVALID_ARG;
-    if (dspark_status s = check_ws(ws, ws_bytes, sizeof(WsHeader))) return s;
-    PlanArgs a{ctx, ell, B, G, P, max_pages, n_pages, table, held, free_list, free_count,
-               static_cast<WsHeader *>(ws), q_start_out, kv_len_out, slot_out, pos_out};
-    return cuda_status(launch_cache_plan(a, static_cast<cudaStream_t>(stream)));
+    const long long T = (long long)B * (G + 1LL);
+    if (T < 0 || T > (1 << 24)) return DSPARK_ERR_INVALID_ARG;
+    return plan({ctx, ell, B, G, P, max_pages, n_pages, table, held, free_list, free_count,
+                 static_cast<WsHeader *>(ws), q_start_out, kv_len_out, slot_out, pos_out, (int)T, nullptr},
+                ws_bytes, stream);
+}
+
+dspark_status dspark_cache_plan_rows(const int32_t *ctx, const int32_t *ell, int B, int G, int P, int max_pages,
+                                     int n_pages, int32_t *table, int32_t *held, const int32_t *free_list,
+                                     int32_t *free_count, int T, void *ws, size_t ws_bytes, int32_t *ell_out,
+                                     int32_t *q_start_out, int32_t *kv_len_out, int32_t *slot_out, int32_t *pos_out,
+                                     void *stream) {
+    if (dspark_status s = injected("dspark_cache_plan_rows")) return s;
+    return plan({ctx, ell, B, G, P, max_pages, n_pages, table, held, free_list, free_count,
+                 static_cast<WsHeader *>(ws), q_start_out, kv_len_out, slot_out, pos_out, T, ell_out},
+                ws_bytes, stream);
 }
 
 dspark_status dspark_cache_commit(const int32_t *ctx, const int32_t *q_start, const int32_t *nout,
@@ -54,13 +79,20 @@ dspark_status dspark_cache_commit(const int32_t *ctx, const int32_t *q_start, co
                                   int32_t *held, int32_t *free_list, int32_t *free_count, void *ws, size_t ws_bytes,
                                   int32_t *ctx_out, void *stream) {
     if (dspark_status s = injected("dspark_cache_commit")) return s;
-    if (!table_ok(B, P, max_pages, n_pages)) return DSPARK_ERR_INVALID_ARG;
-    if (!ctx || !q_start || !nout || !table || !held || !free_list || !free_count || !ctx_out)
-        return DSPARK_ERR_INVALID_ARG;
-    if (dspark_status s = check_ws(ws, ws_bytes, sizeof(WsHeader))) return s;
-    CommitArgs a{ctx, q_start, nout, done, B, P, max_pages, n_pages, table, held, free_list, free_count,
-                 static_cast<WsHeader *>(ws), ctx_out};
-    return cuda_status(launch_cache_commit(a, static_cast<cudaStream_t>(stream)));
+    return commit({ctx, q_start, nout, done, B, P, max_pages, n_pages, table, held, free_list, free_count,
+                   static_cast<WsHeader *>(ws), ctx_out, nullptr, nullptr, nullptr, 0},
+                  ws_bytes, stream);
+}
+
+dspark_status dspark_cache_commit_round(const int32_t *ctx, const int32_t *q_start, int32_t *nout, int32_t *acc,
+                                        int32_t *tokens, const int32_t *done, int B, int G, int P, int max_pages,
+                                        int n_pages, int32_t *table, int32_t *held, int32_t *free_list,
+                                        int32_t *free_count, void *ws, size_t ws_bytes, int32_t *ctx_out,
+                                        void *stream) {
+    if (dspark_status s = injected("dspark_cache_commit_round")) return s;
+    return commit({ctx, q_start, nout, done, B, P, max_pages, n_pages, table, held, free_list, free_count,
+                   static_cast<WsHeader *>(ws), ctx_out, nout, acc, tokens, G},
+                  ws_bytes, stream);
 }
 
 dspark_status dspark_qk_norm_rope(const void *q, long long q_stride, const void *k, long long k_stride,

@@ -79,6 +79,8 @@ struct PlanArgs {
     int32_t *free_count;
     WsHeader *hdr;
     int32_t *q_start, *kv_len, *slot, *pos;
+    int T;              // rows of slot and pos
+    int32_t *ell_out;   // may be ell, or null
 };
 struct CommitArgs {
     const int32_t *ctx, *q_start, *nout, *done;
@@ -86,6 +88,9 @@ struct CommitArgs {
     int32_t *table, *held, *free_list, *free_count;
     WsHeader *hdr;
     int32_t *ctx_out;
+    // A round's results, cleared where a request has no rows (null: left alone).
+    int32_t *nout_rw, *acc, *tokens;
+    int G;
 };
 cudaError_t launch_cache_plan(const PlanArgs &a, cudaStream_t st);
 cudaError_t launch_cache_commit(const CommitArgs &a, cudaStream_t st);

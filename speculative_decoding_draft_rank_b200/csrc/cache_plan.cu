@@ -18,6 +18,9 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kCommitThreads = 1024;
+// Pages (below 2^27) and rows (4096 requests of 2^20 + 1, below 2^33) in one sum.
+constexpr int kRowBits = 34;
+constexpr long long kRowMask = (1LL << kRowBits) - 1;
 
 __device__ __forceinline__ int pages_of(int tokens, int P) { return (tokens + P - 1) / P; }
 
@@ -71,7 +74,7 @@ __device__ __forceinline__ Wish wish_of(const PlanArgs &a, int b, uint32_t &flag
         w.n = w.need = 0;
         return w;
     }
-    int e = __ldg(a.ell + b);
+    int e = a.ell[b];   // ell_out may be ell
     if (e < 0 || e > a.G) {
         flags |= DSPARK_DEV_ELL_RANGE;
         e = min(max(e, 0), a.G);
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
             w.n = max(0, min(w.n, w.held * a.P - w.ctx));
             w.need = 0;
         }
-        both += (long long)w.need << 32 | (unsigned)w.n;
+        both += (long long)w.need << kRowBits | w.n;
         old[b] = w.held;
         start[b] = w.n;
         first[b] = w.need;
@@ -128,11 +131,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
     long long run = block_scan<kPlanThreads>(both, sums, part);
     for (int b = b0; b < b1; ++b) {
         const int n = start[b], nd = first[b];
-        start[b] = (int)run;
-        first[b] = (int)(run >> 32);
-        run += (long long)nd << 32 | (unsigned)n;
+        start[b] = (int)min(run & kRowMask, (long long)a.T);
+        first[b] = (int)(run >> kRowBits);
+        run += (long long)nd << kRowBits | n;
     }
-    const int rows = (int)sums, pages = (int)(sums >> 32);
+    if ((sums & kRowMask) > a.T) flags |= DSPARK_DEV_CACHE_FULL;
+    const int rows = (int)min(sums & kRowMask, (long long)a.T), pages = (int)(sums >> kRowBits);
     if (tid == 0) {
         start[a.B] = rows;
         first[a.B] = pages;
@@ -145,14 +149,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanArgs
         a.q_start[b] = start[b];
         a.kv_len[b] = c < 0 ? 0 : min(c, a.max_pages * a.P) + n;
         a.held[b] = old[b] + first[b + 1] - first[b];
+        if (a.ell_out != nullptr) a.ell_out[b] = max(n - 1, 0);
     }
     if (id == 0) {
         a.q_start[a.B] = rows;
         *a.free_count = count - pages;
     }
     if (rank == 0 && flags) atomicOr(&a.hdr->status, flags);
-    const int T = a.B * (a.G + 1);
-    for (int t = id; t < T; t += stride) {
+    for (int t = id; t < a.T; t += stride) {
         int slot = -1, pos = -1;
         if (t < rows) {
             const int b = owner(start, a.B, t);
@@ -197,10 +201,17 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const Comm
             held = min(max(held, 0), a.max_pages);
         }
         int out = -1;
+        // Nothing of a request without rows went through the target.
+        if (a.nout_rw != nullptr && __ldg(a.q_start + b + 1) <= __ldg(a.q_start + b)) {
+            a.nout_rw[b] = 0;
+            if (a.acc != nullptr) a.acc[b] = 0;
+            if (a.tokens != nullptr)
+                for (int j = 0; j <= a.G; ++j) a.tokens[(size_t)b * (a.G + 1) + j] = -1;
+        }
         if (c >= 0 && (a.done == nullptr || __ldg(a.done + b) == 0)) {
             const int s0 = max(0, __ldg(a.q_start + b)), s1 = max(s0, __ldg(a.q_start + b + 1));
             const int n = min(s1 - s0, a.max_pages * a.P);
-            const int k = __ldg(a.nout + b);
+            const int k = a.nout[b];
             if (k < 0 || k > n) flags |= DSPARK_DEV_LENGTH_RANGE;
             out = min(c, a.max_pages * a.P) + min(max(k, 0), n);
             out = min(out, a.max_pages * a.P);
@@ -241,7 +252,7 @@ cudaError_t launch_cache_plan(const PlanArgs &a, cudaStream_t st) {
     // One CTA for up to 1024 tokens, else a cluster of 8.  Measured, one CTA
     // against the cluster: 24 tokens 3.9 and 4.5 us, 384 4.3 and 4.9, 1152 5.1
     // and 4.9, 2400 6.6 and 5.3.
-    const int ranks = a.B * (a.G + 1) <= 2 * kPlanThreads ? 1 : 8;
+    const int ranks = a.T <= 2 * kPlanThreads ? 1 : 8;
     const size_t bytes = (size_t)(3 * a.B + 3) * sizeof(int);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(cache_plan_kernel), (3 * 4096 + 3) * sizeof(int), done);

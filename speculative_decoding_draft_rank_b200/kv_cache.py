@@ -9,8 +9,9 @@ of seats and orders the library's calls:
   * ``plan(ell)`` after scheduling: rows, positions, slots and pages of the
     round's tokens (the last committed token and ell draft tokens per seat);
   * per layer ``write`` (head norms, rotation, cache write) and ``attend``;
-  * ``commit(nout)`` after verification: the accepted tokens stay, the pages
-    behind them go back to the pool.
+  * ``commit(nout)`` after verification (``commit_round`` on a round's own
+    outputs): the accepted tokens stay, the pages behind them go back to the
+    pool.
 
 ``DeviceRound(..., cache=...)`` and ``ProductionRound`` call plan and commit
 in their places.  Everything runs in libdspark's kernels on the given stream
@@ -69,17 +70,27 @@ class PagedCache:
         self.ws = torch.zeros((need + 255) // 256 * 256, dtype=torch.uint8, device=dev)
 
     # --------------------------------------------------------------- rounds
-    def plan(self, ell, stream=None) -> Rows:
-        """Rows, slots and pages for the round's 1 + ell[b] tokens per seat."""
+    def plan(self, ell, stream=None, ell_out=None) -> Rows:
+        """Rows, slots and pages for the round's 1 + ell[b] tokens per seat.
+        Where pages run out (the pool, or a seat's max_pages) a seat gets fewer
+        rows or none, and the status word says CACHE_FULL; ell_out [B] (may be
+        ell) receives the lengths that the rows cover, for verification."""
         r = self.rows
-        _lib.dspark_cache_plan(self.ctx, ell, r.G, self.table, self.held, self.free_list, self.free_count, self.page,
-                               self.ws, r.q_start, r.kv_len, r.slot, r.pos, stream)
+        _lib.dspark_cache_plan_rows(self.ctx, ell, r.G, self.table, self.held, self.free_list, self.free_count,
+                                    self.page, self.ws, r.q_start, r.kv_len, r.slot, r.pos, ell_out, stream)
         return r
 
     def commit(self, nout, done=None, stream=None):
         """Keep nout[b] of the planned tokens; seats with done[b] are emptied."""
         _lib.dspark_cache_commit(self.ctx, self.rows.q_start, nout, done, self.table, self.held, self.free_list,
                                  self.free_count, self.page, self.ws, self.ctx, stream)
+
+    def commit_round(self, nout, acc=None, tokens=None, done=None, stream=None):
+        """commit after verification on the planned lengths: seats without rows
+        (empty, or no page for their next token) emit nothing -- their nout and
+        acc become 0 and their tokens -1, in place."""
+        _lib.dspark_cache_commit_round(self.ctx, self.rows.q_start, nout, acc, tokens, done, self.table, self.held,
+                                       self.free_list, self.free_count, self.page, self.ws, self.ctx, stream)
 
     def write(self, layer: int, q, k, v, q_out, wq=None, wk=None, rows: Rows | None = None, k_out=None, stream=None):
         """Norm and turn the projections q, k [T, heads, D] of the planned rows

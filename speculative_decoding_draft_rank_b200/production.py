@@ -93,8 +93,7 @@ class ProductionRound:
                                  o["x"], o["pd_x"], o["rowmax"], o["rowsum"], st)
         _lib.dspark_confidence(t["h"], t["w"], float(dr.inp.bias), t["tau"], o["c"], o["S"], st)
         self.sched.select(o["S"], o["ell"], o["n_adm"], o["order"], st)
-        if dr.cache is not None:
-            dr.cache.plan(o["ell"], st)
+        dr.plan(st)
         if dr.target is not None:
             dr.target(dr, st)
         _lib.dspark_verify(t["Tlog"], t["L"], t["U"], t["Wt"], t["x0"], o["x"], o["pd_x"], o["rowmax"],

@@ -30,7 +30,10 @@ class DeviceRound:
         the round's dtype); None drafts with the Markov head.
         cache: a kv_cache.PagedCache of this batch; the round then plans its
         rows after scheduling and commits the emitted counts after
-        verification.  target(round, stream): enqueues the target pass between
+        verification.  A request whose pages run out is verified on the tokens
+        that its rows cover (o["ell"] is cut to them); one without rows emits
+        nothing (nout = 0, tokens -1), and device_status() says CACHE_FULL.
+        target(round, stream): enqueues the target pass between
         the two (its logits go to t["Tlog"], rows 0..ell of each request);
         None takes the logits as they are (run_from_host takes the host's)."""
         if cache is not None and (cache.B != inp.B or cache.G < inp.G):
@@ -116,8 +119,7 @@ class DeviceRound:
             conf(main)
         _lib.dspark_schedule(o["S"], t["knots_n"], t["knots_t"], self.budget, self.mode, self.ws, o["ell"],
                              o["n_adm"], o["theta"], o["order"], main)
-        if self.cache is not None:
-            self.cache.plan(o["ell"], main)
+        self.plan(main)
         if verify:
             if self.target is not None:
                 self.target(self, main)
@@ -181,10 +183,18 @@ class DeviceRound:
                                o["rowsum"], t["temp"], t["u_accept"], t["u_final"], o["ell"], self.ws, o["acc"],
                                o["tokens"], o["nout"], o["pt_x"], stream)
 
-    def commit(self, stream=None):
-        """Keep the emitted tokens' keys and values in the cache, if there is one."""
+    def plan(self, stream=None):
+        """Rows and pages of the admitted tokens in the cache, if there is one;
+        o["ell"] becomes the lengths that got their rows."""
         if self.cache is not None:
-            self.cache.commit(self.o["nout"], None, stream)
+            self.cache.plan(self.o["ell"], stream, ell_out=self.o["ell"])
+
+    def commit(self, stream=None):
+        """Keep the emitted tokens' keys and values in the cache, if there is
+        one; requests without rows emit nothing."""
+        if self.cache is not None:
+            o = self.o
+            self.cache.commit_round(o["nout"], o["acc"], o["tokens"], None, stream)
 
     def upload(self, stream=None):
         """Copy every input from pinned host memory (end-to-end timing)."""
@@ -209,7 +219,9 @@ class DeviceRound:
         return {k: v.cpu().numpy() for k, v in self.o.items()}
 
     def device_status(self) -> int:
-        return _lib.dspark_get_device_status(self.ws)
+        """Data errors so far, the cache's among them."""
+        st = _lib.dspark_get_device_status(self.ws)
+        return st if self.cache is None else st | self.cache.device_status()
 
 
 class _null:

@@ -161,3 +161,34 @@ def test_attention_takes_long_prompts(lib):
         assert _attend(lib, **{**dict(n=1 << 20, qs=8192, ws=None, out=ctypes.c_void_p(1 << 45)), **ok}) == 3, ok
     for bad in (dict(B=1, T=1 << 21, Hq=64, Hkv=8, P=64, mp=1 << 15), dict(B=4096, T=1 << 24, Hq=64, Hkv=8, P=128, mp=8192)):
         assert _attend(lib, **{**dict(n=1 << 20, qs=8192, ws=None, out=ctypes.c_void_p(1 << 45)), **bad}) == 1, bad
+
+
+def test_plan_rows_and_commit_round_refusals(lib, monkeypatch):
+    def plan(B=4, G=5, P=64, mp=8, n=100, T=24, ws=WS, wsb=256, null=None):
+        p = [A] * 10
+        if null is not None:
+            p[null] = None
+        return lib.dspark_cache_plan_rows(p[0], p[1], B, G, P, mp, n, p[2], p[3], p[4], p[5], T, ws, wsb, None, p[6],
+                                          p[7], p[8], p[9], None)
+
+    def commit(B=4, G=5, P=64, mp=8, n=100, ws=WS, wsb=256, null=None):
+        p = [A] * 8
+        if null is not None:
+            p[null] = None
+        return lib.dspark_cache_commit_round(p[0], p[1], p[2], None, None, None, B, G, P, mp, n, p[3], p[4], p[5], p[6],
+                                             ws, wsb, p[7], None)
+
+    for bad in (dict(B=0), dict(B=4097), dict(G=-1), dict(G=(1 << 20) + 1), dict(P=48), dict(mp=0), dict(n=0)):
+        assert plan(**bad) == 1 and commit(**bad) == 1, bad
+    assert plan(T=-1) == 1 and plan(T=(1 << 24) + 1) == 1
+    for k in range(10):
+        assert plan(null=k) == 1, k
+    for k in range(8):
+        assert commit(null=k) == 1, k
+    assert plan(T=0, null=8, ws=None) == 3 and plan(T=0, null=9, ws=None) == 3      # no rows, no arrays
+    assert plan(B=4096, G=1 << 20, ws=None) == 3
+    assert plan(wsb=255) == 3 and commit(ws=None) == 3 and commit(wsb=0) == 3
+    monkeypatch.setenv("DSPARK_INJECT_ERROR", "dspark_cache_plan_rows=4")
+    assert plan() == 4
+    monkeypatch.setenv("DSPARK_INJECT_ERROR", "dspark_cache_commit_round=4")
+    assert commit() == 4

@@ -544,3 +544,60 @@ def test_attention_of_a_long_prompt(B, n, L):
     # the reciprocal and the product in fp32, then half a step of bf16
     assert ((out[:n].double() - ref).abs() <= ref * (2.0 ** -8 + 2.0 ** -22)).all()
     assert (out[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("B,G,T,max_pages,pool", [(5, 5, 12, 9, 30), (5, 5, 300, 9, 30), (300, 4, 1100, 8, 700),
+                                                  (4096, 3, 9000, 3, 5000), (3, 70, 0, 20, 30), (64, 1 << 20, 2500, 8, 300)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_of_any_number_of_rows(B, G, T, max_pages, pool, in_place):
+    """Arrays shorter or longer than the batch's rows, and the lengths that the rows cover."""
+    P = 16
+    rng = np.random.default_rng(B + T)
+    t = oc.Tables(B, max_pages, rng.permutation(pool).tolist())
+    d = DeviceTables(t, pool, B, 0, P)
+    d.slot, d.pos = _i32([7] * T), _i32([7] * T)
+    ctx = np.where(rng.random(B) < 0.2, -1, rng.integers(0, 9, B))
+    ell = rng.integers(0, min(G, 60) + 1, B)
+    ell_d = _i32(ell)
+    granted = ell_d if in_place else _i32([7] * B)
+    # contexts that are there already
+    for b, x in enumerate(ctx):
+        if x > 0 and t.free:
+            t.rows[b].append(t.free.pop())
+    d.table, d.held = _i32(t.table()), _i32([len(r) for r in t.rows])
+    d.free, d.count = _i32(t.free + [-1] * (pool - len(t.free))), _i32([len(t.free)])
+    _lib.dspark_cache_plan_rows(_i32(ctx), ell_d, G, d.table, d.held, d.free, d.count, P, d.ws, d.q_start, d.kv, d.slot,
+                                d.pos, ell_out=granted)
+    start, kv, slot, pos, full = t.plan(ctx.tolist(), ell.tolist(), min(G, 60), P)
+    m = start[-1]
+    slot, pos = slot[:m], pos[:m]
+    cut = np.minimum(start, T)
+    n = np.diff(cut)
+    d.check(t)
+    assert d.q_start.tolist() == cut.tolist()
+    assert d.kv.tolist() == np.where(ctx < 0, 0, ctx + n).tolist()
+    assert d.slot.tolist() == (slot + [-1] * T)[:T] and d.pos.tolist() == (pos + [-1] * T)[:T]
+    assert granted.tolist() == np.maximum(n - 1, 0).tolist()
+    assert _lib.dspark_get_device_status(d.ws) == (_lib.DEV_CACHE_FULL if full or m > T else 0)
+
+
+def test_commit_of_a_round_clears_requests_without_rows():
+    t = oc.Tables(4, 2, list(range(6)))
+    d = DeviceTables(t, 6, 4, 2, 16)
+    ctx = [3, -1, 32, 0]
+    t.rows = [[5], [], [4, 3], []]
+    t.free = [0, 1, 2]
+    d.table, d.held = _i32(t.table()), _i32([1, 0, 2, 0])
+    d.free, d.count = _i32([0, 1, 2, -1, -1, -1]), _i32([3])
+    d.plan(_i32(ctx), _i32([2, 0, 1, 0]))
+    start, *_ = t.plan(ctx, [2, 0, 1, 0], 2, 16)
+    _lib.dspark_clear_device_status(d.ws)
+    nout, acc = _i32([2, 1, 2, 1]), _i32([1, 0, 1, 0])
+    tokens = _i32([[5, 6, -1], [7, -1, -1], [8, 9, -1], [4, -1, -1]])
+    _lib.dspark_cache_commit_round(_i32(ctx), d.q_start, nout, acc, tokens, None, d.table, d.held, d.free, d.count, 16,
+                                   d.ws, d.ctx_out)
+    assert nout.tolist() == [2, 0, 0, 1] and acc.tolist() == [1, 0, 0, 0]
+    assert tokens.tolist() == [[5, 6, -1], [-1] * 3, [-1] * 3, [4, -1, -1]]
+    assert d.ctx_out.tolist() == t.commit(ctx, start, [2, 0, 0, 1], None, 16) == [5, -1, 32, 1]
+    d.check(t)
+    assert _lib.dspark_get_device_status(d.ws) == 0

@@ -247,3 +247,60 @@ def test_round_refuses_a_cache_of_another_batch():
         DeviceRound(inp, kn, kt, -1, 1, cache=PagedCache(3, 2, 1, 2, 2, 64, n_pages=6, max_pages=4, page=16))
     with pytest.raises(ValueError):
         DeviceRound(inp, kn, kt, -1, 1, cache=PagedCache(4, 1, 1, 2, 2, 64, n_pages=6, max_pages=4, page=16))
+
+
+@pytest.mark.parametrize("how", ["run", "host", "production"])
+def test_a_round_whose_pages_run_out(how):
+    """One free page and a seat at max_pages: requests are verified on the rows they got, a seat without rows emits
+    nothing, and tokens and cache stay together.  The target fills the planned rows only; the others hold other logits."""
+    from speculative_decoding_draft_rank_b200.production import ProductionRound, ProductionScheduler
+    B, G, V, r, d, P = 8, 4, 4096, 32, 64, 16
+    kn, kt = np.array([0, 64], np.int32), np.array([8.0, 8.1])
+    inp = synth.generate(B, G, V, r, d, "bf16", seed=6, hot=8)
+    lengths = [30, 1, 17, 16, 5, 64, 0, 47]
+    c = PagedCache(B, G, 1, 4, 2, 64, n_pages=15, max_pages=4, page=P, inv_freq=_freq(64))
+    t = oc.Tables(B, 4, list(range(14, -1, -1)))
+    c.admit(lengths)
+    ctx = [x if x else -1 for x in lengths]
+    t.plan([0 if x else -1 for x in lengths], [max(x - 1, 0) for x in lengths], 63, P)
+    plain = DeviceRound(inp, kn, kt, -1, 1)
+    true = plain.t["Tlog"].clone()
+    stale = true.roll(1, -1)
+
+    def target(dr, stream):
+        n = (c.rows.q_start[1:] - c.rows.q_start[:-1])[:, None]
+        fresh = torch.arange(G + 1, device="cuda") < n
+        dr.t["Tlog"].copy_(torch.where(fresh[..., None], true, dr.t["Tlog"]))
+
+    dr = DeviceRound(inp, kn, kt, -1, 1, pinned_host=how == "host", cache=c, target=None if how == "host" else target)
+    if how == "production":
+        run = ProductionRound(dr, ProductionScheduler(B, G, kn, kt)).run
+        ref = ProductionRound(plain, ProductionScheduler(B, G, kn, kt)).run
+    else:
+        run, ref = dr.run_from_host if how == "host" else dr.run, plain.run
+    starved = short = 0
+    for _ in range(3):
+        dr.t["Tlog"].copy_(stale)
+        run()
+        ref()
+        ell = plain.o["ell"].tolist()
+        start, kv, slot, pos, full = t.plan(ctx, ell, G, P)
+        n = np.diff(start)
+        plain.o["ell"].copy_(_i32(np.maximum(n - 1, 0)))
+        plain.verify()
+        torch.cuda.synchronize()
+        a, b = dr.outputs(), plain.outputs()
+        assert full and c.rows.slot.tolist() == slot and c.rows.q_start.tolist() == start
+        assert a["ell"].tolist() == np.maximum(n - 1, 0).tolist()
+        for k in ("acc", "tokens", "nout"):
+            assert np.array_equal(a[k][n > 0], b[k][n > 0]), k
+        assert (a["nout"][n == 0] == 0).all() and (a["acc"][n == 0] == 0).all() and (a["tokens"][n == 0] == -1).all()
+        if how == "host":
+            for k in ("ell", "tokens", "nout"):
+                assert np.array_equal(dr.host_out[k].numpy(), a[k])
+        starved += sum(int(m == 0 and x >= 0) for m, x in zip(n, ctx))
+        short += sum(int(0 < m < e + 1) for m, e in zip(n, ell))
+        ctx = t.commit(ctx, start, a["nout"].tolist(), None, P)
+        assert c.ctx.tolist() == ctx and c.free_list[: int(c.free_count)].tolist() == t.free
+        assert dr.device_status() == _lib.DEV_CACHE_FULL
+    assert starved > 0 and short > 0
