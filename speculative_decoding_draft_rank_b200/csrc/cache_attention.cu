@@ -162,6 +162,11 @@ constexpr int kItemCost = 70, kMinQuota = 16;   // a quota holds the start of at
 constexpr long long kRefused = 1LL << 50;
 __device__ __forceinline__ int item_cost(const Block &k) { return k.nt * tile_cost(k) + kItemCost; }
 
+// x / d, short where x is: 64-bit divisions take some two hundred cycles.
+__device__ __forceinline__ unsigned long long divide(unsigned long long x, uint32_t d) {
+    return x >> 32 == 0 ? (uint32_t)x / d : x / d;
+}
+
 // The item in which position `pos` of the batch's costs lies, its first tile
 // that starts there or later (nt: none), and the tiles of the batch before that.
 struct Spot {
@@ -192,7 +197,7 @@ __device__ __forceinline__ Spot spot_at(const AttnArgs &a, const long long *cost
         rest -= all;
         p.tiles += p.k.nt * a.Hkv;
     }
-    p.h = (int)(rest / c);
+    p.h = (int)divide(rest, c);
     const int off = (int)(rest - (unsigned long long)p.h * c);
     p.start = 0u - off;
     const int w = tile_cost(p.k);
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
     // positions of a run can count: nothing is done.
     const bool refused = total > (long long)gridDim.x * INT_MAX;
     if (refused && tid == 0 && blockIdx.x == 0) flag_status(a.hdr, DSPARK_DEV_LENGTH_RANGE);
-    const int quota = refused ? INT_MAX : max(kMinQuota, (int)((total + gridDim.x - 1) / gridDim.x));
+    const int quota = refused ? INT_MAX : max(kMinQuota, (int)divide(total + gridDim.x - 1, gridDim.x));
     const long long w0 = (long long)blockIdx.x * quota, w1 = w0 + quota;
     Spot spot = {};
     int tiles = 0;
