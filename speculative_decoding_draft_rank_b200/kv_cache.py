@@ -36,6 +36,11 @@ class Rows:
         self.slot = torch.full((self.T,), -1, **i32)
         self.pos = torch.full((self.T,), -1, **i32)
 
+    def used_on(self, stream):
+        """Keep the arrays' memory from reuse until `stream` has done what it was given so far."""
+        for t in (self.q_start, self.kv_len, self.slot, self.pos):
+            t.record_stream(stream)
+
 
 class PagedCache:
     """B seats, `n_layers` layers of Hkv key heads read by Hq query heads of
@@ -92,18 +97,24 @@ class PagedCache:
         _lib.dspark_cache_commit_round(self.ctx, self.rows.q_start, nout, acc, tokens, done, self.table, self.held,
                                        self.free_list, self.free_count, self.page, self.ws, self.ctx, stream)
 
+    def _rows(self, rows, stream) -> Rows:
+        if rows is None or rows is self.rows:
+            return self.rows
+        rows.used_on(torch.cuda.current_stream(self.device) if stream is None else stream)
+        return rows
+
     def write(self, layer: int, q, k, v, q_out, wq=None, wk=None, rows: Rows | None = None, k_out=None, stream=None):
         """Norm and turn the projections q, k [T, heads, D] of the planned rows
         and put keys and values v into the layer's cache; queries come back in
         q_out (which may be q), keys in k_out where it is given."""
-        r = self.rows if rows is None else rows
+        r = self._rows(rows, stream)
         _lib.dspark_qk_norm_rope(q, k, wq, wk, self.eps, r.pos, self.inv_freq, self.interleaved, r.n_rows, q_out,
                                  k_out, self.ws, v=v, cache=self.layers[layer], slot=r.slot, page=self.page,
                                  k_scale=self.k_scale, v_scale=self.v_scale, stream=stream)
 
     def attend(self, layer: int, q, out, rows: Rows | None = None, stream=None):
         """out [T, Hq, D] = attention of the rows q over the layer's cache."""
-        r = self.rows if rows is None else rows
+        r = self._rows(rows, stream)
         _lib.dspark_cache_attention(q, self.layers[layer], self.table, r.q_start, r.kv_len, self.page, self.scale,
                                     self.window, self.ws, out, k_scale=self.k_scale, v_scale=self.v_scale,
                                     stream=stream)
@@ -114,15 +125,19 @@ class PagedCache:
                                v_scale=self.v_scale, stream=stream)
 
     # -------------------------------------------------------------- prompts
-    def admit(self, lengths) -> Rows:
+    def admit(self, lengths, stream=None) -> Rows:
         """Seat prompts: lengths[b] > 0 tokens into empty seat b (0: no
         change).  Returns the rows to run the prompt pass on (write and attend
         with rows=...); the tokens count as cached from here on.  Raises if a
         seat is taken or the pool is too small, leaving the cache as it was.
-        Waits for the device."""
+        Waits for the device before (rounds and graph replays on any stream
+        have then left the tables) and after (any stream may go on from here);
+        runs on `stream`, by default the current one.  No call on this cache
+        may be made from another thread meanwhile."""
         want = torch.as_tensor(lengths, dtype=torch.int32).cpu()
         if want.shape != (self.B,) or int(want.min()) < 0 or int(want.max()) == 0:
             raise ValueError(f"lengths: {self.B} prompt lengths, one of them positive")
+        torch.cuda.synchronize(self.device)
         ctx = self.ctx.cpu()
         if bool(((want > 0) & (ctx >= 0)).any()):
             raise ValueError("a prompt for a seat that is taken")
@@ -130,14 +145,17 @@ class PagedCache:
         if need > int(self.free_count) or int(want.max()) > self.table.shape[1] * self.page:
             raise RuntimeError(f"the prompts need {need} pages, {int(self.free_count)} are free, "
                                f"{self.table.shape[1]} at most per seat")
-        r = Rows(self.B, int(want.max()) - 1, self.device)
-        new = (want > 0).to(self.device)
-        want = want.to(self.device)
-        none = torch.full_like(want, -1)
-        _lib.dspark_cache_plan(torch.where(new, 0, none), (want - 1).clamp(min=0), r.G, self.table, self.held,
-                               self.free_list, self.free_count, self.page, self.ws, r.q_start, r.kv_len, r.slot,
-                               r.pos)
-        self.ctx.copy_(torch.where(new, want, self.ctx))
+        st = torch.cuda.current_stream(self.device) if stream is None else stream
+        with torch.cuda.stream(st):
+            r = Rows(self.B, int(want.max()) - 1, self.device)
+            new = (want > 0).to(self.device)
+            want = want.to(self.device)
+            none = torch.full_like(want, -1)
+            _lib.dspark_cache_plan(torch.where(new, 0, none), (want - 1).clamp(min=0), r.G, self.table, self.held,
+                                   self.free_list, self.free_count, self.page, self.ws, r.q_start, r.kv_len, r.slot,
+                                   r.pos, st)
+            self.ctx.copy_(torch.where(new, want, self.ctx))
+        torch.cuda.synchronize(self.device)
         return r
 
     def device_status(self) -> int:

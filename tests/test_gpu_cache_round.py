@@ -304,3 +304,42 @@ def test_a_round_whose_pages_run_out(how):
         assert c.ctx.tolist() == ctx and c.free_list[: int(c.free_count)].tolist() == t.free
         assert dr.device_status() == _lib.DEV_CACHE_FULL
     assert starved > 0 and short > 0
+
+
+def test_admit_between_rounds_on_another_stream():
+    """Rounds on a side stream that lags behind the host, admission from the default stream: admit sees what the last
+    commit left, and the next round sees what admit did."""
+    B, G, P = 3, 2, 16
+    c = PagedCache(B, G, 1, 2, 1, 64, n_pages=12, max_pages=4, page=P, inv_freq=_freq(64))
+    t = oc.Tables(B, 4, list(range(11, -1, -1)))
+    side = torch.cuda.Stream()
+
+    def seat(lengths, ctx, **kw):
+        rows = c.admit(lengths, **kw)
+        t.plan([0 if x else -1 for x in lengths], [max(x - 1, 0) for x in lengths], max(lengths) - 1, P)
+        m = Model(c, rows.T, 1)
+        side.wait_stream(torch.cuda.current_stream())
+        m.run(c, rows, stream=side)
+        side.synchronize()
+        m.check(c, rows, t.table())
+        return [x or y for x, y in zip(lengths, ctx)]
+
+    ctx = seat([30, 5, 0], [-1, -1, -1])
+    for rnd in range(3):
+        ell, nout = _i32([2, 1, 0]), _i32([2, 1, 1])
+        done = _i32([b == rnd for b in range(B)])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        c.plan(ell, stream=side)
+        c.commit(nout, done, stream=side)
+        start, *_ = t.plan(ctx, [2, 1, 0], G, P)
+        ctx = t.commit(ctx, start, [2, 1, 1], [b == rnd for b in range(B)], P)
+        # the seat that the commit under way empties
+        ctx = seat([30 if b == rnd else 0 for b in range(B)], ctx, **({"stream": side} if rnd == 2 else {}))
+        c.plan(_i32([0, 0, 0]), stream=side)
+        side.synchronize()
+        start, kv, slot, *_ = t.plan(ctx, [0, 0, 0], G, P)
+        assert c.ctx.tolist() == ctx and c.rows.kv_len.tolist() == kv and c.rows.slot.tolist() == slot
+        assert c.free_list[: int(c.free_count)].tolist() == t.free
+    assert c.device_status() == 0
