@@ -25,16 +25,20 @@ from . import _lib
 
 
 class Rows:
-    """The packed rows of one plan: request b has rows q_start[b] .. q_start[b + 1] of arrays with `T` rows."""
+    """The packed rows of one plan: request b has rows q_start[b] .. q_start[b + 1] of arrays with `T` rows
+    (by default as many as any plan can give; slot and pos may be longer, -1 behind the last row)."""
 
-    def __init__(self, B: int, G: int, device):
+    MOST = 1 << 24     # rows that a plan or a pass takes
+
+    def __init__(self, B: int, G: int, device, T: int | None = None):
         i32 = dict(dtype=torch.int32, device=device)
-        self.B, self.G, self.T = B, G, B * (G + 1)
+        self.B, self.G, self.T = B, G, B * (G + 1) if T is None else T
         self.q_start = torch.zeros(B + 1, **i32)
         self.n_rows = self.q_start[B:]
         self.kv_len = torch.zeros(B, **i32)
-        self.slot = torch.full((self.T,), -1, **i32)
-        self.pos = torch.full((self.T,), -1, **i32)
+        entries = self.T if T is None else max(T, min(B * (G + 1), self.MOST))
+        self.slot = torch.full((entries,), -1, **i32)
+        self.pos = torch.full((entries,), -1, **i32)
 
     def used_on(self, stream):
         """Keep the arrays' memory from reuse until `stream` has done what it was given so far."""
@@ -128,8 +132,10 @@ class PagedCache:
     def admit(self, lengths, stream=None) -> Rows:
         """Seat prompts: lengths[b] > 0 tokens into empty seat b (0: no
         change).  Returns the rows to run the prompt pass on (write and attend
-        with rows=...); the tokens count as cached from here on.  Raises if a
-        seat is taken or the pool is too small, leaving the cache as it was.
+        with rows=..., on arrays of rows.T rows, the prompts' tokens); the
+        tokens count as cached from here on.  At most 2^20 tokens a prompt and
+        2^24 a call.  Raises if a seat is taken or the pool is too small,
+        leaving the cache as it was.
         Waits for the device before (rounds and graph replays on any stream
         have then left the tables) and after (any stream may go on from here);
         runs on `stream`, by default the current one.  No call on this cache
@@ -137,6 +143,9 @@ class PagedCache:
         want = torch.as_tensor(lengths, dtype=torch.int32).cpu()
         if want.shape != (self.B,) or int(want.min()) < 0 or int(want.max()) == 0:
             raise ValueError(f"lengths: {self.B} prompt lengths, one of them positive")
+        total = int(want.sum(dtype=torch.int64))
+        if total > Rows.MOST or int(want.max()) > 1 << 20:
+            raise ValueError(f"{total} prompt tokens, the longest {int(want.max())}: at most 2^24 a call, 2^20 a prompt")
         torch.cuda.synchronize(self.device)
         ctx = self.ctx.cpu()
         if bool(((want > 0) & (ctx >= 0)).any()):
@@ -147,13 +156,13 @@ class PagedCache:
                                f"{self.table.shape[1]} at most per seat")
         st = torch.cuda.current_stream(self.device) if stream is None else stream
         with torch.cuda.stream(st):
-            r = Rows(self.B, int(want.max()) - 1, self.device)
+            r = Rows(self.B, int(want.max()) - 1, self.device, total)
             new = (want > 0).to(self.device)
             want = want.to(self.device)
             none = torch.full_like(want, -1)
-            _lib.dspark_cache_plan(torch.where(new, 0, none), (want - 1).clamp(min=0), r.G, self.table, self.held,
-                                   self.free_list, self.free_count, self.page, self.ws, r.q_start, r.kv_len, r.slot,
-                                   r.pos, st)
+            _lib.dspark_cache_plan_rows(torch.where(new, 0, none), (want - 1).clamp(min=0), r.G, self.table, self.held,
+                                        self.free_list, self.free_count, self.page, self.ws, r.q_start, r.kv_len,
+                                        r.slot, r.pos, stream=st)
             self.ctx.copy_(torch.where(new, want, self.ctx))
         torch.cuda.synchronize(self.device)
         return r

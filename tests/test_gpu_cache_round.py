@@ -343,3 +343,50 @@ def test_admit_between_rounds_on_another_stream():
         assert c.ctx.tolist() == ctx and c.rows.kv_len.tolist() == kv and c.rows.slot.tolist() == slot
         assert c.free_list[: int(c.free_count)].tolist() == t.free
     assert c.device_status() == 0
+
+
+def test_a_long_prompt_in_a_cache_of_many_seats():
+    """Rows are the prompts' tokens, not seats times the longest prompt."""
+    B, P, D, Hq = 256, 128, 64, 2
+    lengths = [0] * B
+    lengths[9], lengths[200] = 37, 70000
+    c = PagedCache(B, 4, 1, Hq, 1, D, n_pages=600, max_pages=560, page=P, inv_freq=_freq(D))
+    rows = c.admit(lengths)
+    assert rows.T == 70037 and rows.slot.numel() >= rows.T
+    assert rows.q_start.tolist() == [0] * 10 + [37] * 191 + [70037] * 56
+    m = Model(c, rows.T, 2)
+    m.run(c, rows)
+    slot = rows.slot[: rows.T].cpu().numpy()
+    q, k, v = (_np(x) for x in m.qkv[0].split([Hq, 1, 1], 1))
+    cache = c.layers[0].cpu().numpy()
+    gk, gv = oc.read(cache, slot, P, D)
+    assert np.array_equal(gv, oc.dequantise(*oc.quantise(v)))
+    at = np.array([0, 36, 37, 38, 165, 40000, 70035, 70036])            # rows as requests of one token each
+    seat = np.where(at < 37, 9, 200)
+    pos = np.where(at < 37, at, at - 37)
+    assert rows.pos[torch.from_numpy(at).cuda()].tolist() == pos.tolist()
+    ref, lim = oc.attention(_np(m.q[0])[at], cache, c.table.cpu().numpy()[seat], np.arange(len(at) + 1), pos + 1, P, c.scale)
+    out = _np(m.out[0])[at]
+    assert (np.abs(out - ref) <= lim * (1 + 2.0 ** -7) + np.abs(ref) * 2.0 ** -8).all()
+    assert c.ctx.tolist() == [x or -1 for x in lengths] and c.device_status() == 0
+    c.commit(_i32([0] * B), _i32([1] * B))
+    assert int(c.free_count) == 600
+    for bad in ([1 << 21] + [0] * (B - 1), [1 << 20] * 17 + [0] * (B - 17)):
+        with pytest.raises(ValueError):
+            c.admit(bad)
+
+
+def test_many_seats_filled_at_once():
+    """4096 prompts of 5000 tokens would be 2^24 padded rows and more; half the seats take short ones."""
+    B, P = 4096, 16
+    lengths = np.zeros(B, int)
+    lengths[::2] = 1 + np.arange(B // 2) % 40
+    lengths[1] = 5000
+    c = PagedCache(B, 4, 1, 2, 1, 64, n_pages=9000, max_pages=320, page=P)
+    rows = c.admit(lengths)
+    t = oc.Tables(B, 320, list(range(8999, -1, -1)))
+    start, kv, slot, pos, full = t.plan(np.where(lengths > 0, 0, -1).tolist(), np.maximum(lengths - 1, 0).tolist(), 4999, P)
+    assert not full and rows.T == lengths.sum() == start[-1]
+    assert rows.slot[: rows.T].tolist() == slot[: rows.T] and rows.pos[: rows.T].tolist() == pos[: rows.T]
+    assert (rows.slot[rows.T:] == -1).all() and rows.q_start.tolist() == start and rows.kv_len.tolist() == kv
+    assert c.device_status() == 0
