@@ -172,7 +172,7 @@ def attention(q, cache, table, q_start, kv_len, P, scale, window=0, kg=1.0, vg=1
     out = np.zeros((q_start[-1], Hq, D))
     bound = np.zeros_like(out)
     for b in range(len(kv_len)):
-        n, L = q_start[b + 1] - q_start[b], kv_len[b]
+        n, L = int(q_start[b + 1]) - int(q_start[b]), int(kv_len[b])
         if n == 0 or L == 0:
             continue
         t = np.arange(L)

@@ -1,5 +1,6 @@
 // abi_cache.cu -- the extern "C" entry points of the target pass's cache and
 // attention: host-side argument checks, then the launchers.
+#include <algorithm>
 #include <cmath>
 
 #include "abi_util.cuh"
@@ -183,7 +184,7 @@ dspark_status dspark_cache_attention(const void *q, long long q_stride, const vo
     a.P = P;
     a.max_pages = max_pages;
     a.n_pages = n_pages;
-    a.window = window;
+    a.window = std::min(window, max_pages * P);   // no table holds more; positions less a window stay in 32 bits
     a.qk_mul = scale * k_scale * kLog2e;
     a.v_mul = v_scale;
     a.out = static_cast<__nv_bfloat16 *>(out);

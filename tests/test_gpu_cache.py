@@ -601,3 +601,12 @@ def test_commit_of_a_round_clears_requests_without_rows():
     assert d.ctx_out.tolist() == t.commit(ctx, start, [2, 0, 0, 1], None, 16) == [5, -1, 32, 1]
     d.check(t)
     assert _lib.dspark_get_device_status(d.ws) == 0
+
+
+@pytest.mark.parametrize("window", [0, 1 << 20, (1 << 31) - 5, (1 << 31) - 1])
+def test_attention_windows_wider_than_the_context(window):
+    """Five tokens of a request that holds one or three: the first have negative positions and see nothing."""
+    rng = np.random.default_rng(12)
+    cache, table = _fill(rng, 3, 1, 64, 16, [1, 3, 200])
+    q = rng.standard_normal((15, 2, 64))
+    _check_attention(q, cache, table, [5, 5, 5], [1, 3, 200], 16, 0.125, window)
