@@ -471,8 +471,9 @@ dspark_status dspark_cache_commit_round(const int32_t *ctx, const int32_t *q_sta
  *          unused for rot = 0); n_rows: device int32 (q_start + B) or NULL
  *          for all T.  Rows from *n_rows on are left alone.
  * Outputs: q_out [T, Hq, D], k_out [T, Hkv, D] dtype, dense; q_out may be q
- *          and k_out may be k where those are dense.  k_out may be NULL when
- *          cache is given.
+ *          and k_out may be k where those are dense, and otherwise they lie
+ *          outside the spans of q, k, v and of each other
+ *          (DSPARK_ERR_INVALID_ARG).  k_out may be NULL when cache is given.
  * Cache:   NULL, or the layer's cache: y of the keys and v go to slot[t]
  *          (negative: nowhere).  Two rows must not name one slot.  NaN is
  *          stored as 0 and infinities as the largest value

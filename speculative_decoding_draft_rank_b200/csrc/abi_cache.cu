@@ -26,6 +26,21 @@ bool rows_ok(const void *p, long long stride, int heads, int D, int dtype) {
     return aligned16(p) && stride >= (long long)heads * D && stride % per == 0;
 }
 
+// `T` tokens of `heads` heads, `stride` elements apart: the bytes they span.
+struct Span {
+    uintptr_t lo, hi;
+    bool dense;   // nothing between the tokens
+};
+Span span_of(const void *p, int T, long long stride, int heads, int D, int dtype) {
+    const long long e = dtype == DSPARK_BF16 ? 2 : 4, row = (long long)heads * D;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + (uintptr_t)(((T - 1) * stride + row) * e), T == 1 || stride == row};
+}
+bool disjoint(const Span &a, const Span &b) { return a.hi <= b.lo || b.hi <= a.lo; }
+// An output over an input: the same dense rows (a thread reads its own rows
+// before it writes them), or apart.
+bool in_place_or_apart(const Span &out, const Span &in) { return disjoint(out, in) || (in.dense && out.lo == in.lo); }
+
 dspark_status plan(const PlanArgs &a, size_t ws_bytes, void *stream) {
     if (!table_ok(a.B, a.P, a.max_pages, a.n_pages) || a.G < 0 || a.G > (1 << 20) || a.T < 0 || a.T > (1 << 24))
         return DSPARK_ERR_INVALID_ARG;
@@ -120,6 +135,15 @@ dspark_status dspark_qk_norm_rope(const void *q, long long q_stride, const void 
     }
     if (dspark_status s = check_ws(ws, ws_bytes, sizeof(WsHeader))) return s;
     if (T == 0) return DSPARK_OK;
+    const Span sq = span_of(q, T, q_stride, Hq, D, dtype), sk = span_of(k, T, k_stride, Hkv, D, dtype);
+    const Span oq = span_of(q_out, T, (long long)Hq * D, Hq, D, dtype);
+    if (!in_place_or_apart(oq, sq) || !disjoint(oq, sk)) return DSPARK_ERR_INVALID_ARG;
+    if (k_out) {
+        const Span ok = span_of(k_out, T, (long long)Hkv * D, Hkv, D, dtype);
+        if (!in_place_or_apart(ok, sk) || !disjoint(ok, sq) || !disjoint(ok, oq)) return DSPARK_ERR_INVALID_ARG;
+        if (cache && !disjoint(ok, span_of(v, T, v_stride, Hkv, D, dtype))) return DSPARK_ERR_INVALID_ARG;
+    }
+    if (cache && !disjoint(oq, span_of(v, T, v_stride, Hkv, D, dtype))) return DSPARK_ERR_INVALID_ARG;
     NormArgs a{q, k, v, q_stride, k_stride, v_stride, wq, wk, eps, pos, inv_freq, rot, interleaved ? 1 : 0, n_rows,
                T, Hq, Hkv, D, dtype, q_out, k_out, static_cast<uint8_t *>(cache), slot, P, n_pages, k_scale, v_scale,
                static_cast<WsHeader *>(ws)};

@@ -610,3 +610,24 @@ def test_attention_windows_wider_than_the_context(window):
     cache, table = _fill(rng, 3, 1, 64, 16, [1, 3, 200])
     q = rng.standard_normal((15, 2, 64))
     _check_attention(q, cache, table, [5, 5, 5], [1, 3, 200], 16, 0.125, window)
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_norm_in_place_beside_its_neighbours(T):
+    """In place on rows that share one buffer: a single token's slices, and stacked dense arrays."""
+    g = torch.Generator().manual_seed(T)
+    Hq, Hkv, D = 4, 2, 64
+    flat = torch.randn(T * (Hq + 2 * Hkv) * D, generator=g).bfloat16().cuda()
+    q, k, v = (x.view(T, -1, D) for x in flat.split([T * Hq * D, T * Hkv * D, T * Hkv * D]))
+    pos, freq = _i32(range(T)), torch.rand(32, generator=g).cuda()
+    ref = torch.empty_like(q), torch.empty_like(k)
+    caches = [_cache(1, Hkv, 16, D) for _ in range(2)]
+    ws = _ws()
+    for (qo, ko), cache in zip((ref, (q, k)), caches):
+        _lib.dspark_qk_norm_rope(q, k, None, None, EPS1, pos, freq, False, None, qo, ko, ws, v=v, cache=cache, slot=pos,
+                                 page=16)
+    assert torch.equal(q, ref[0]) and torch.equal(k, ref[1]) and torch.equal(*caches)
+    with pytest.raises(_lib.DsparkError):
+        _lib.dspark_qk_norm_rope(q, k, None, None, EPS1, pos, freq, False, None, q, v, ws, v=v, cache=caches[0], slot=pos,
+                                 page=16)
+    assert _lib.dspark_get_device_status(ws) == 0
