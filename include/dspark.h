@@ -511,7 +511,9 @@ dspark_status dspark_cache_read(const void *cache, const int32_t *slot, int T, i
  *          (max_pages * P / 8 + 102) < 2^38 (a prompt of 2^20 tokens at 64
  *          query heads is two thirds of it).
  * fp32 scores, maxima and sums; probabilities enter the second product in
- * f16, keys, values and queries exactly.  Any n_b and any group Hq / Hkv.
+ * f16 (half a step is 2^-11 of them, or 2^-32 of the row's largest), keys and
+ * values exactly, queries exactly down to 2^-31 of their row's largest element
+ * (rows above 2^-86).  Any n_b and any group Hq / Hkv.
  * Deterministic.  Two launches.  bf16 only (DSPARK_ERR_UNSUPPORTED_DTYPE). */
 size_t dspark_cache_attention_workspace_size(int B, int Hq, int Hkv, int D);
 dspark_status dspark_cache_attention(const void *q, long long q_stride, const void *cache, const int32_t *table,

@@ -193,7 +193,7 @@ def attention(q, cache, table, q_start, kv_len, P, scale, window=0, kg=1.0, vg=1
                 dx = D * 2.0 ** -23 * (np.abs(kk) @ np.abs(qq)).max() * abs(scale) + 2.0 ** -21 + \
                     2.0 ** -22 * np.abs(x - x.max()).max()
                 # probabilities: half an f16 step each in the numerator and the sum, the score error twice, the
-                # fp32 sums, and f16's smallest step (2^-25 of the largest) where p is subnormal
+                # fp32 sums, and half of f16's smallest step, 2^-32 of the largest (lifted by 2^7), where p is subnormal
                 rel = 2 * (2.0 ** -11 + dx) + len(p) * 2.0 ** -23
-                bound[q_start[b] + j, h] = rel * (p @ np.abs(vv)) + 2 * len(p) * 2.0 ** -25 * p.max() * np.abs(vv).max()
+                bound[q_start[b] + j, h] = rel * (p @ np.abs(vv)) + 2 * len(p) * 2.0 ** -32 * p.max() * np.abs(vv).max()
     return out, bound

@@ -38,10 +38,15 @@
 // A thread copies the codes of its own key with cp.async, one own tile ahead,
 // so no barrier stands between copy and use.  (A producer warp with two bulk
 // copies per page took 2200 cycles a tile: it was what bounded the kernel.)
-// P is exp2 of the scaled score minus a running maximum that is only raised
-// (and O, L rescaled) when a score passes it by more than 8, so P <= 256 and
-// f16 keeps its 11 bits; K, V and Q (scaled by a power of two per row) are
-// exact in f16, so P's rounding is the only one before the output's.
+// P is 2^7 times exp2 of the scaled score minus a running maximum that is only
+// raised (and O, L rescaled) when a score passes it by more than 8.  So P is at
+// most 2^15; f16 keeps 11 bits of it down to 2^-21 of the maximum, then steps
+// of 2^-31, and drops a key below 2^-32 (half a step) from both sums: n such
+// keys lose less than n * 2^-32 of the row.  K and V are exact in f16.  Q is
+// scaled by a power of two per row to [2^14, 2^15) (rows above 2^-86); its
+// elements are exact down to 2^-31 of the row's largest, and smaller ones off
+// by 2^-39 of it at most.  So P's rounding is the only one that counts before
+// the output's.
 //
 // Measured: 1450-1900 cycles a tile (18 KB of cache) where HBM would need 800.
 // A tile moves 1200 (32 rows) to 1350 (48 rows) x 128 bytes through shared
@@ -73,7 +78,8 @@ constexpr int kWarpLoad = 4 * kGroups, kWarpQk = kWarpLoad + 1, kWarpPv = kWarpL
 constexpr int kThreads = (kWarpLoad + 4) * 32;
 constexpr int kMaxCtas = 160;
 constexpr long long kWaitBudget = 4000000000LL;
-constexpr float kRaise = 8.f;     // log2 room above the running maximum
+constexpr float kLift = 7.f;      // log2 of P at the running maximum
+constexpr float kRaise = 15.f;    // and of the largest P before the maximum is raised
 constexpr int kDescInts = 8;      // CTAs that go on with the item, q0, r0, nr, h
 
 // TMEM columns.
@@ -93,7 +99,8 @@ struct Lay {
 };
 
 // What the softmax knows of an item's rows, two rows to an entry of `mul_m`:
-// the multipliers of their raw scores and their negated running maxima.
+// the multipliers of their raw scores and their negated running maxima, which
+// are kept kLift low throughout, in the parts for the join too.
 struct Rows {
     float4 mul_m[kRows / 2];
     int2 lim[kRows];         // visible keys [x, y)
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                                 if (me < l.x || me >= l.y) x = -INFINITY;
                             }
                             x = warp_max_f32(x);
-                            if (lane == 0) rw.neg_max(r0 + i) = x == x ? -x : INFINITY;
+                            if (lane == 0) rw.neg_max(r0 + i) = x == x ? kLift - x : INFINITY;
                         }
                     }
                     __syncwarp();
@@ -682,8 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_kernel(const Attn
                         if (key < N) {
                             float &neg = rw.neg_max(key);
                             const float old = -neg;
-                            const float nm = fmaxf(fmaxf(fmaxf(ms.wmax[sg][0][key], ms.wmax[sg][1][key]),
-                                                         fmaxf(ms.wmax[sg][2][key], ms.wmax[sg][3][key])), old);
+                            const float top = fmaxf(fmaxf(ms.wmax[sg][0][key], ms.wmax[sg][1][key]),
+                                                    fmaxf(ms.wmax[sg][2][key], ms.wmax[sg][3][key]));
+                            const float nm = fmaxf(top - kLift, old);
                             ms.fac[sg][key] = nm == old ? 1.f : fast_exp2(old - nm);
                             neg = -nm;
                         }

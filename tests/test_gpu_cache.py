@@ -631,3 +631,32 @@ def test_norm_in_place_beside_its_neighbours(T):
         _lib.dspark_qk_norm_rope(q, k, None, None, EPS1, pos, freq, False, None, q, v, ws, v=v, cache=caches[0], slot=pos,
                                  page=16)
     assert _lib.dspark_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("down", [20.0, 22.5, 24.4, 25.6, 28.0])
+def test_attention_of_one_key_over_a_flat_tail(down):
+    """The first key's weight is 2^down times every other's, its value is 0, and one CTA has the whole context: the
+    result is what the tail adds up to.  A weight is off by half a step of f16 at 2^7 times its size: 2^-32, or 2^-11
+    of itself."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    D, P, pages = 64, 128, 1024
+    N = pages * P - 1
+    rec = _lib.dspark_cache_record_bytes(P, D)
+    k, v = np.zeros((pages * P, 1, D)), np.full((pages * P, 1, D), 6.0)
+    k[0, 0, 0], v[0] = 6.0, 0.0
+    cache = np.zeros((pages, 1, rec), np.uint8)
+    one = np.zeros((3, 1, rec), np.uint8)
+    oc.write(one, np.arange(2 * P), k[:2 * P], v[:2 * P], P)
+    cache[0], cache[1:] = one[0], one[1]
+    q = torch.zeros(sms, 2, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 4.0
+    out = torch.zeros_like(q)
+    ws = _ws(_lib.dspark_cache_attention_workspace_size(sms, 2, 1, D))
+    _lib.dspark_cache_attention(q, torch.from_numpy(cache).cuda(), _i32(np.tile(np.arange(pages), (sms, 1))),
+                                _i32(np.arange(sms + 1)), _i32([pages * P] * sms), P, down * np.log(2.0) / 24, 0, ws, out)
+    assert _lib.dspark_get_device_status(ws) == 0
+    w = 2.0 ** -down
+    ref = 6.0 * N * w / (1 + N * w)
+    # ... the scale's and the score's rounding in fp32 (down * 2^-22), the output's half step
+    tol = 6.0 * N * max(2.0 ** -32, w * 2.0 ** -11) + ref * (down * 2.0 ** -22 + 2.0 ** -8)
+    assert (out.double() - ref).abs().max().item() <= tol
