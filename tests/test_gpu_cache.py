@@ -660,3 +660,44 @@ def test_attention_of_one_key_over_a_flat_tail(down):
     # ... the scale's and the score's rounding in fp32 (down * 2^-22), the output's half step
     tol = 6.0 * N * max(2.0 ** -32, w * 2.0 ** -11) + ref * (down * 2.0 ** -22 + 2.0 ** -8)
     assert (out.double() - ref).abs().max().item() <= tol
+
+
+def _near_border(x, grid):
+    """Is x within 2^-22 of a midpoint of the grid (where rounding the divisor to fp32 may turn the code)?"""
+    mid = (grid[1:] + grid[:-1]) / 2
+    i = np.clip(np.searchsorted(mid, x), 1, len(mid) - 1)
+    return np.minimum(np.abs(x - mid[i]), np.abs(x - mid[i - 1])) <= x * 2.0 ** -22
+
+
+@pytest.mark.parametrize("kg,vg", [(0.3, 1.7e-5), (1.0 / 3, 12345.678), (6.1e-17, 9.9e18)])
+def test_cache_with_layer_scales_of_any_value(kg, vg):
+    """Layer scales that are no powers of two: 6 g and scale * g round to fp32, so a code may turn at a border only."""
+    T, Hkv, D, P = 200, 2, 128, 32
+    kg, vg = float(np.float32(kg)), float(np.float32(vg))
+    gen = torch.Generator().manual_seed(13)
+    k, v = ((torch.randn(T, Hkv, D, generator=gen) * torch.exp(torch.randn(T, Hkv, 1, generator=gen)) * g).cuda()
+            for g in (kg, vg))
+    slot, ws, cache = _i32(np.random.default_rng(0).permutation(256)[:T]), _ws(), _cache(8, Hkv, P, D)
+    _lib.dspark_qk_norm_rope(k, k, None, None, EPS1, None, None, False, None, torch.empty_like(k), None, ws, v=v,
+                             cache=cache, slot=slot, page=P, k_scale=kg, v_scale=vg)
+    out = torch.empty_like(k), torch.empty_like(v)
+    _lib.dspark_cache_read(cache, slot, P, *out, ws, k_scale=kg, v_scale=vg)
+    assert _lib.dspark_get_device_status(ws) == 0
+    stored = oc.read(cache.cpu().numpy(), slot.cpu().numpy(), P, D)
+    for x, g, y, o in zip((_np(k), _np(v)), (kg, vg), stored, out):
+        code, sc = oc.quantise(x, g)
+        off = (y != oc.dequantise(code, sc)).reshape(T, Hkv, -1, 16)
+        top = np.abs(x).reshape(T, Hkv, -1, 16).max(-1) / (6 * g)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            near = _near_border(np.abs(x).reshape(off.shape) / (oc.E4M3[sc] * g)[..., None], oc.GRID)
+        assert not (off & ~near & ~_near_border(top, oc.E4M3[:127])[..., None]).any()
+        assert off.mean() < 1e-3
+        assert (np.abs(_np(o) - y * g) <= np.abs(y * g) * 2.0 ** -24).all()
+
+
+def test_attention_layer_scales_of_any_value():
+    rng = np.random.default_rng(14)
+    kg, vg = float(np.float32(0.3)), float(np.float32(7.7))
+    cache, table = _fill(rng, 2, 2, 64, 16, [300, 77], kg=kg, vg=vg)
+    q = rng.standard_normal((5, 4, 64))
+    _check_attention(q, cache, table, [2, 3], [300, 77], 16, 0.4, kg=kg, vg=vg)
