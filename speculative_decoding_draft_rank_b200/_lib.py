@@ -352,7 +352,7 @@ def _rows(t, dev, what):
     s0, s1, s2 = t.stride()
     if s2 != 1 or (H > 1 and s1 != D):
         raise ValueError(f"{what}: the heads of a token must be dense")
-    return t.data_ptr(), (s0 if T > 1 else max(s0, H * D))
+    return t.data_ptr(), (s0 if T > 1 else H * D)   # of a single token the stride says nothing
 
 
 def _launch(fn, dev, stream, *args):

@@ -205,3 +205,15 @@ def test_norm_refuses_outputs_over_other_rows(lib):
                 dict(cache=at(0x80000), slot=at(0x70000), qo=at(0x20000)),
                 dict(cache=at(0x80000), slot=at(0x70000), ko=at(0x20000))):
         assert _norm(lib, **{**far, **bad}) == 1, bad
+
+
+def test_stride_of_a_single_token():
+    """One token of a projection whose rows are not 16-byte multiples: there is no second row to be misaligned."""
+    wide = torch.zeros(3, 4 * 64 + 3, dtype=torch.bfloat16)
+    one = wide[:1, : 4 * 64].view(1, 4, 64)
+    assert one.stride(0) % 8 != 0
+    assert _lib._rows(one, one.get_device(), "q") == (one.data_ptr(), 256)
+    two = wide[:2, : 4 * 64].view(2, 4, 64)
+    assert _lib._rows(two, two.get_device(), "q") == (two.data_ptr(), 259)
+    with pytest.raises(ValueError):
+        _lib._rows(wide[:2, :128].view(2, 2, 64)[:, :, ::2], -1, "q")
