@@ -210,10 +210,11 @@ def test_norm_refuses_outputs_over_other_rows(lib):
 def test_stride_of_a_single_token():
     """One token of a projection whose rows are not 16-byte multiples: there is no second row to be misaligned."""
     wide = torch.zeros(3, 4 * 64 + 3, dtype=torch.bfloat16)
-    one = wide[:1, : 4 * 64].view(1, 4, 64)
+    heads = wide[:, : 4 * 64].unflatten(1, (4, 64))
+    one = heads[:1]
     assert one.stride(0) % 8 != 0
     assert _lib._rows(one, one.get_device(), "q") == (one.data_ptr(), 256)
-    two = wide[:2, : 4 * 64].view(2, 4, 64)
+    two = heads[:2]
     assert _lib._rows(two, two.get_device(), "q") == (two.data_ptr(), 259)
     with pytest.raises(ValueError):
-        _lib._rows(wide[:2, :128].view(2, 2, 64)[:, :, ::2], -1, "q")
+        _lib._rows(two[:, :, ::2], two.get_device(), "q")
