@@ -479,7 +479,8 @@ dspark_status dspark_cache_commit_round(const int32_t *ctx, const int32_t *q_sta
  *          stored as 0 and infinities as the largest value
  *          (DSPARK_DEV_BAD_VALUE).
  * Limits:  D = 64 or 128, rot a multiple of 32 up to D, Hq a multiple of Hkv,
- *          Hq <= 1024, T <= 2^24.  fp32 inside, one rounding at the end. */
+ *          Hq <= 1024, T <= 2^24.  fp32 inside, the sum of squares too (norms
+ *          of |x| up to 2^60), one rounding at the end. */
 dspark_status dspark_qk_norm_rope(const void *q, long long q_stride, const void *k, long long k_stride,
                                   const void *v, long long v_stride, const void *wq, const void *wk, float eps,
                                   const int32_t *pos, const float *inv_freq, int rot, int interleaved,

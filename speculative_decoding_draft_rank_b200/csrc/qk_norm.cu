@@ -16,11 +16,16 @@
 // loads and stores are 16 bytes.  The angles are reduced to a turn in fp64 (a
 // position of 2^20 times a frequency has 44 bits), then sine and cosine run in
 // fp32 once per token and frequency, shared by all heads.
-// Measured (bf16, D = 128): 920 tokens of 64 query and 8 key heads (46 MB)
-// 19 us, 5200 tokens of 32 and 8 (141 MB with the read back) 45 us, one token
-// 3 us in a graph; reading the same tokens back 6.5, 12 and 2.5 us.  HBM would
-// need 7 and 21 us: what bounds the large ones is instruction issue, not
-// bytes, hence two-lane fp32 arithmetic and several rows per thread.
+// Measured (bf16, D = 128, with the cache write): 1184 tokens of 64 query and 8
+// key heads (45 MB) 14 us, 5200 tokens of 32 and 8 (113 MB) 39 us with the rows
+// in L2 and 45 from HBM, one token 3 to 4 us in a graph; HBM alone would need 7
+// and 17 us.  Reading the same tokens back takes 3.1, 6.4 and 2 us (0.9 and 4.2).
+// What bounds the large ones: four CTAs of 128 threads fit an SM (104 to 124
+// registers), and a token's positions, angles and first rows are waited for
+// before its arithmetic begins, so time goes up by waves of 592 tokens (592
+// tokens 8.0 us, 740 12.7, 1184 14.3); inside a wave the schedulers issue in
+// 53 % of the cycles (hence two-lane fp32 arithmetic and several rows a
+// thread), at 20 % of DRAM's rate.
 #include "cache.cuh"
 
 namespace dspark {
