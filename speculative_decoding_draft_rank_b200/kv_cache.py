@@ -110,7 +110,8 @@ class PagedCache:
     def write(self, layer: int, q, k, v, q_out, wq=None, wk=None, rows: Rows | None = None, k_out=None, stream=None):
         """Norm and turn the projections q, k [T, heads, D] of the planned rows
         and put keys and values v into the layer's cache; queries come back in
-        q_out (which may be q), keys in k_out where it is given."""
+        q_out (which may be q where that is contiguous), keys in k_out where it
+        is given."""
         r = self._rows(rows, stream)
         _lib.dspark_qk_norm_rope(q, k, wq, wk, self.eps, r.pos, self.inv_freq, self.interleaved, r.n_rows, q_out,
                                  k_out, self.ws, v=v, cache=self.layers[layer], slot=r.slot, page=self.page,

@@ -249,7 +249,7 @@ def test_round_refuses_a_cache_of_another_batch():
         DeviceRound(inp, kn, kt, -1, 1, cache=PagedCache(4, 1, 1, 2, 2, 64, n_pages=6, max_pages=4, page=16))
 
 
-@pytest.mark.parametrize("how", ["run", "host", "production"])
+@pytest.mark.parametrize("how", ["run", "host", "production", "graph"])
 def test_a_round_whose_pages_run_out(how):
     """One free page and a seat at max_pages: requests are verified on the rows they got, a seat without rows emits
     nothing, and tokens and cache stay together.  The target fills the planned rows only; the others hold other logits."""
@@ -278,6 +278,13 @@ def test_a_round_whose_pages_run_out(how):
         ref = ProductionRound(plain, ProductionScheduler(B, G, kn, kt)).run
     else:
         run, ref = dr.run_from_host if how == "host" else dr.run, plain.run
+    if how == "graph":
+        ref()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            dr.run()
+        run = graph.replay
     starved = short = 0
     for _ in range(3):
         dr.t["Tlog"].copy_(stale)
