@@ -144,7 +144,7 @@ struct AttnArgs {
 size_t attention_ws_bytes(int D);
 // The most work a call may bring, in the kernel's units (at most 16 a tile of
 // 128 keys, 70 an item of up to 48 rows): positions inside a CTA's share are
-// 32 bits, and a share is 1/148 of this.  (About four minutes of a GPU.)
+// 32 bits, and a share is 1/148 of this.  (About two minutes of a GPU.)
 inline bool attention_work_fits(int B, int T, int Hkv, int group, int P, int max_pages) {
     const double items = (double)Hkv * ((double)B + (double)T * group / 48.0 + 1.0);
     return items * (16.0 * ((double)max_pages * P / 128.0 + 2.0) + 70.0) < 0x1p38;

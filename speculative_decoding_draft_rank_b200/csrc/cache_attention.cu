@@ -49,8 +49,8 @@
 // the output's.
 //
 // Measured: 256 requests of up to 6 tokens over 4096, 64 heads over 8, 350 us;
-// 4 requests over 131072, 32 heads over 8, 136 to 170 us (by the lengths and
-// the box); 128 requests of up to 17 tokens, window 128, 55 us; one token 16.
+// 4 requests over 131072, 32 heads over 8, 136 to 170 (by the lengths drawn);
+// 128 requests of up to 17 tokens, window 128, 55; one token 16.
 // From a capture of the first (44 thousand tiles of 18 KB): 2150 cycles a CTA
 // and tile, changes of items among them, where HBM would need 800; 4200 warp
 // instructions and 820 wavefronts of shared-memory loads and stores a tile

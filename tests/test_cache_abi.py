@@ -201,7 +201,7 @@ def test_norm_refuses_outputs_over_other_rows(lib):
     for bad in (dict(qo=at(16)), dict(qo=at(0x10000)), dict(qo=at(0x10000 - 8192 + 16)), dict(ko=at(0)), dict(ko=at(0x10010)),
                 dict(ko=at(0x30000 + 8176)), dict(ko=at(0x30000 - 4080)),
                 dict(qs=2048, qo=at(0)), dict(ks=1024, ko=at(0x10000)),            # in place, but not dense
-                dict(q=at(0), k=at(2048), v=at(3072), qs=2048, ks=2048, vs=2048, qo=at(4 * 4096 - 2064)),
+                dict(q=at(0), k=at(2048), v=at(2048 + 1024), qs=2048, ks=2048, vs=2048, qo=at(4 * 4096 - 2064)),
                 dict(cache=at(0x80000), slot=at(0x70000), qo=at(0x20000)),
                 dict(cache=at(0x80000), slot=at(0x70000), ko=at(0x20000))):
         assert _norm(lib, **{**far, **bad}) == 1, bad
